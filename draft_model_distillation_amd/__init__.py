@@ -4,7 +4,7 @@ The computation lives in hand-written gfx950 HIP kernels behind the C ABI of inc
 (libopd_mi355x.so, built by ``draft_model_distillation_amd.build``). This package only binds it:
 
     opd_loss_fwd, opd_loss_bwd, verify_accept_len, opd_fused_fwd_bwd_verify, verify_sample,
-    lmhead_fused_fwd_bwd_verify
+    lmhead_fused_fwd_bwd_verify, adjust_logits, topk_rows, topk_loss_fwd, topk_loss_bwd, topk_fused_fwd_bwd
 
 take torch device tensors and enqueue on torch's current stream.
 """
@@ -14,11 +14,15 @@ from ._binding import (  # noqa: F401
     CapacityEstimate,
     OPD_BF16,
     OPD_F32,
+    OPD_FLAG_BAD_LIST,
     OPD_FLAG_BAD_OFFSETS,
     OPD_FLAG_BAD_TOKEN,
+    OPD_FLAG_EMPTY_MASK,
     OPD_FLAG_NEG_L,
     OPD_FLAG_SPIN_TIMEOUT,
+    OPD_TOPK_MAX,
     OpdError,
+    adjust_logits,
     check_mode,
     debug_reserve_flags,
     length_head_loss,
@@ -34,6 +38,10 @@ from ._binding import (  # noqa: F401
     set_check,
     set_spin_limit,
     stream_probe,
+    topk_fused_fwd_bwd,
+    topk_loss_bwd,
+    topk_loss_fwd,
+    topk_rows,
     verify_accept_len,
     verify_sample,
     workspace,

@@ -7,6 +7,7 @@ built this module raises instead of computing anything another way.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -20,6 +21,10 @@ OPD_FLAG_NEG_L = 1
 OPD_FLAG_BAD_OFFSETS = 2
 OPD_FLAG_SPIN_TIMEOUT = 4
 OPD_FLAG_BAD_TOKEN = 8
+OPD_FLAG_BAD_LIST = 16
+OPD_FLAG_EMPTY_MASK = 32
+OPD_TOPK_MAX = 256
+OPD_KL = {"reverse": 0, "forward": 1}
 
 EXPORTED_SYMBOLS = (
     "opd_workspace_size",
@@ -33,6 +38,13 @@ EXPORTED_SYMBOLS = (
     "opd_verify_sample",
     "opd_lmhead_scratch_size",
     "opd_lmhead_fused_fwd_bwd_verify",
+    "opd_adjust_logits",
+    "opd_topk_scratch_size",
+    "opd_topk_rows",
+    "opd_topk_loss_scratch_size",
+    "opd_topk_loss_fwd",
+    "opd_topk_loss_bwd",
+    "opd_topk_fused_fwd_bwd",
     "opd_capacity_init",
     "opd_capacity_observe",
     "opd_pack_first_fit",
@@ -48,6 +60,16 @@ EXPORTED_SYMBOLS = (
 
 class OpdBlocks(ctypes.Structure):
     _fields_ = [("offsets", ctypes.c_void_p), ("L", ctypes.c_void_p), ("n_blocks", ctypes.c_int32)]
+
+
+class OpdAdjust(ctypes.Structure):
+    _fields_ = [("offsets", ctypes.c_void_p), ("n_blocks", ctypes.c_int32), ("draft_tokens", ctypes.c_void_p),
+                ("history", ctypes.c_void_p), ("ld_history", ctypes.c_int64), ("max_history", ctypes.c_int32),
+                ("history_len", ctypes.c_void_p), ("prompt_len", ctypes.c_void_p), ("repetition", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p), ("bias_tokens", ctypes.c_void_p),
+                ("bias_values", ctypes.c_void_p), ("ld_bias", ctypes.c_int64), ("max_bias", ctypes.c_int32),
+                ("bias_len", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("ld_mask", ctypes.c_int64),
+                ("n_masks", ctypes.c_int32), ("mask_row", ctypes.c_void_p), ("masked_value", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -110,6 +132,21 @@ def load_library(require_torch_runtime: bool = True) -> ctypes.CDLL:
         lib.opd_lmhead_fused_fwd_bwd_verify.argtypes = [vp, vp, i64, vp, i32, i64, i64, i64, ctypes.POINTER(OpdBlocks),
                                                         ctypes.c_float, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp,
                                                         vp, vp, vp, sz, i64, vp, sz, vp]
+        lib.opd_adjust_logits.restype = i32
+        lib.opd_adjust_logits.argtypes = [vp, i32, i64, i64, i64, ctypes.POINTER(OpdAdjust), vp, i64, vp, sz, vp]
+        lib.opd_topk_scratch_size.restype = sz
+        lib.opd_topk_scratch_size.argtypes = [i64, i64, i32, ctypes.c_int32]
+        lib.opd_topk_rows.restype = i32
+        lib.opd_topk_rows.argtypes = [vp, i32, i64, i64, i64, ctypes.c_int32, vp, vp, vp, vp, sz, vp, sz, vp]
+        lib.opd_topk_loss_scratch_size.restype = sz
+        lib.opd_topk_loss_scratch_size.argtypes = [i64, i64, i32]
+        top = [vp, i32, i64, i64, i64, vp, vp, ctypes.c_int32, vp, i32, f32, f32]
+        lib.opd_topk_loss_fwd.restype = i32
+        lib.opd_topk_loss_fwd.argtypes = top + [vp, vp, vp, sz, vp, sz, vp]
+        lib.opd_topk_loss_bwd.restype = i32
+        lib.opd_topk_loss_bwd.argtypes = top + [vp, vp, vp, i32, i64, vp, sz, vp]
+        lib.opd_topk_fused_fwd_bwd.restype = i32
+        lib.opd_topk_fused_fwd_bwd.argtypes = top + [vp, vp, vp, vp, i32, i64, vp, sz, vp, sz, vp]
         lib.opd_stream_probe.restype = i32
         lib.opd_stream_probe.argtypes = [vp, vp, vp, sz, vp]
         lib.opd_set_spin_limit.restype = None
@@ -700,3 +737,257 @@ def opd_fused_fwd_bwd_verify_noalloc(z, y, offsets, lengths, alpha: float, tau: 
         out["accept_len"].data_ptr() if n_blocks else None, _stream(dev))
     _check("opd_fused_fwd_bwd_verify_noalloc", st)
     return out
+
+
+def _table(t, name: str, rows: int, dtype):
+    """(columns, pitch) of a 2-D [rows, n] table of `dtype` whose rows may be padded."""
+    _require(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
+    _require(t.dim() == 2 and t.shape[0] == rows, f"{name} must be [{rows}, n], got {tuple(t.shape)}")
+    _require(t.shape[1] <= 1 or t.stride(1) == 1, f"{name} must have unit stride along its rows")
+    _require(rows <= 1 or t.stride(0) >= t.shape[1], f"{name}: rows must not overlap")
+    return int(t.shape[1]), int(t.stride(0)) if rows > 1 else int(max(t.stride(0), t.shape[1]))
+
+
+def _device_guard(dev):
+    """Launches go to the current device, which need not be the tensors'."""
+    torch = _torch()
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def adjust_logits(x, offsets, history=None, history_len=None, prompt_len=None, draft_tokens=None, repetition=None,
+                  frequency=None, presence=None, bias_tokens=None, bias_values=None, bias_len=None, mask=None,
+                  mask_row=None, masked_value: float = -1.0e4, out=None, ws=None):
+    """Penalties, biases and grammar masks on the rows of packed blocks (opd_adjust_logits).
+
+    x [R, V] fp32 or bf16; offsets [B + 1] int32: rows of each request. Optional: history [B, n] int32
+    with history_len [B] and prompt_len [B] int32; draft_tokens [R] int32 (each row also sees the
+    proposals of its block's earlier rows); repetition, frequency, presence [B] f32; bias_tokens [B, m]
+    int32 and bias_values [B, m] f32 with bias_len [B] int32 (of a token listed twice the last entry
+    counts); mask [M, ceil(V / 32)] int32 words, bit set = allowed, with mask_row [R] int32 (negative:
+    none; without it row r has mask r). A masked logit becomes masked_value; the row kernels of this
+    library want finite logits, so use -inf only in front of code of your own.
+
+    Returns the adjusted logits: a new tensor, or ``out``, which may be x itself. Rows outside every block are
+    left as they are in ``out`` (unspecified in a new tensor).
+    """
+    torch = _torch()
+    xp, rows, vocab, ld = _matrix(x, "x")
+    dt = _dtype_code(x)
+    _require(offsets.dim() == 1 and offsets.numel() >= 1, "offsets must be a 1-D tensor of n_blocks + 1 entries")
+    n_blocks = int(offsets.numel()) - 1
+    _vector(offsets, "offsets", n_blocks + 1, torch.int32)
+    _vector(draft_tokens, "draft_tokens", rows, torch.int32, optional=True)
+    for name, t in (("repetition", repetition), ("frequency", frequency), ("presence", presence)):
+        _vector(t, name, n_blocks, torch.float32, optional=True)
+    a = OpdAdjust(offsets.data_ptr(), n_blocks, _ptr(draft_tokens))
+    a.repetition, a.frequency, a.presence = _ptr(repetition), _ptr(frequency), _ptr(presence)
+    if history is None:
+        _require(history_len is None and prompt_len is None, "history_len and prompt_len need history")
+    else:
+        a.max_history, a.ld_history = _table(history, "history", n_blocks, torch.int32)
+        _vector(history_len, "history_len", n_blocks, torch.int32)
+        _vector(prompt_len, "prompt_len", n_blocks, torch.int32, optional=True)
+        if a.max_history:  # (an empty table has no address)
+            a.history, a.history_len, a.prompt_len = history.data_ptr(), history_len.data_ptr(), _ptr(prompt_len)
+    if bias_tokens is None:
+        _require(bias_values is None and bias_len is None, "bias_values and bias_len need bias_tokens")
+    else:
+        _require(bias_values is not None, "bias_values is required")
+        a.max_bias, a.ld_bias = _table(bias_tokens, "bias_tokens", n_blocks, torch.int32)
+        m, ld_values = _table(bias_values, "bias_values", n_blocks, torch.float32)
+        _require((m, ld_values) == (a.max_bias, a.ld_bias), "bias_tokens and bias_values must have the same layout")
+        _vector(bias_len, "bias_len", n_blocks, torch.int32)
+        if m:
+            a.bias_tokens, a.bias_values, a.bias_len = (t.data_ptr() for t in (bias_tokens, bias_values, bias_len))
+    if mask is None:
+        _require(mask_row is None, "mask_row needs mask")
+    else:
+        _require(mask.dim() == 2, "mask must be 2-D")
+        a.n_masks = int(mask.shape[0])
+        words, a.ld_mask = _table(mask, "mask", a.n_masks, torch.int32)
+        _require(words >= (vocab + 31) // 32, f"mask must have {(vocab + 31) // 32} words per row, got {words}")
+        _vector(mask_row, "mask_row", rows, torch.int32, optional=True)
+        _require(mask_row is not None or a.n_masks >= rows, "one mask per row is needed without mask_row")
+        if a.n_masks:
+            a.mask, a.mask_row = mask.data_ptr(), _ptr(mask_row)
+    a.masked_value = float(masked_value)
+    if out is not None:
+        _require(out.dtype == x.dtype, f"out must be {x.dtype}, got {out.dtype}")
+        op, rows_o, vocab_o, ld_o = _matrix(out, "out", whole_vectors=False)
+        _require((rows_o, vocab_o) == (rows, vocab), f"out must be [{rows}, {vocab}], got {tuple(out.shape)}")
+        if (op, ld_o) != (xp, ld):
+            _no_overlap(out, x, "out", "x")
+    dev = x.device
+    _same_device(dev, [("offsets", offsets), ("draft_tokens", draft_tokens), ("history", history),
+                       ("history_len", history_len), ("prompt_len", prompt_len), ("repetition", repetition),
+                       ("frequency", frequency), ("presence", presence), ("bias_tokens", bias_tokens),
+                       ("bias_values", bias_values), ("bias_len", bias_len), ("mask", mask), ("mask_row", mask_row),
+                       ("out", out)])
+    lib = load_library()
+    with _device_guard(dev):
+        ws = _workspace_arg(ws, dev)
+        if out is None:
+            out = _empty_rows(rows, vocab, x.dtype, dev)
+            op, _, _, ld_o = _matrix(out, "out", whole_vectors=False)
+        st = lib.opd_adjust_logits(xp, dt, rows, vocab, ld, ctypes.byref(a), op, ld_o, ws.data_ptr(), ws.numel(),
+                                   _stream(dev))
+    _check("opd_adjust_logits", st)
+    return out
+
+
+def _scratch_arg(scratch, need: int, dev):
+    """The caller's scratch where it is large enough, else a new one (None where none is needed)."""
+    if need and (scratch is None or scratch.numel() * scratch.element_size() < need):
+        return _torch().empty(need, dtype=_torch().uint8, device=dev)
+    return scratch
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def topk_rows(y, k: int, scratch=None, ws=None, out=None) -> dict:
+    """The k largest logits of every row and the log-sum-exp of its others (opd_topk_rows).
+
+    Returns values [R, k] f32 (falling), index [R, k] int32 (equal logits by rising index) and rest_lse
+    [R] f32: together a row's distribution over its top tokens and, as one class, all the others.
+    ``out`` may hold preallocated tensors under the same keys and ``scratch`` a contiguous device tensor
+    of at least opd_topk_scratch_size bytes.
+    """
+    torch = _torch()
+    yp, rows, vocab, ld = _matrix(y, "y")
+    dt = _dtype_code(y)
+    k = int(k)
+    _require(1 <= k <= min(OPD_TOPK_MAX, vocab), f"k must be in [1, {min(OPD_TOPK_MAX, vocab)}], got {k}")
+    o = dict(out) if out is not None else {}
+    if o:
+        for name, dtype in (("values", torch.float32), ("index", torch.int32)):
+            _require(o.get(name) is not None, f"out[{name!r}] is missing")
+            _rows_matrix(o[name], name, rows, k, dtype)
+        _vector(o.get("rest_lse"), "rest_lse", rows, torch.float32)
+    _require(scratch is None or scratch.is_contiguous(), "scratch must be contiguous")
+    dev = y.device
+    _same_device(dev, [("scratch", scratch)] + [(n, o.get(n)) for n in ("values", "index", "rest_lse")])
+    lib = load_library()
+    with _device_guard(dev):
+        ws = _workspace_arg(ws, dev)
+        scratch = _scratch_arg(scratch, lib.opd_topk_scratch_size(rows, vocab, dt, k), dev)
+        if not o:
+            o["values"] = torch.empty(rows, k, dtype=torch.float32, device=dev)
+            o["index"] = torch.empty(rows, k, dtype=torch.int32, device=dev)
+            o["rest_lse"] = torch.empty(rows, dtype=torch.float32, device=dev)
+        st = lib.opd_topk_rows(yp, dt, rows, vocab, ld, k, o["values"].data_ptr(), o["index"].data_ptr(),
+                               o["rest_lse"].data_ptr(), _ptr(scratch), _nbytes(scratch), ws.data_ptr(), ws.numel(),
+                               _stream(dev))
+    _check("opd_topk_rows", st)
+    return o
+
+
+def _topk_loss_args(z, top_index, top_logit, rest_lse, alpha, tau, kl):
+    """Checks the arguments the three calls share; returns (leading C arguments, rows, vocab,
+    the teacher's tensors by name, for the device check)."""
+    torch = _torch()
+    zp, rows, vocab, ld = _matrix(z, "z")
+    dt = _dtype_code(z)
+    _require(top_index.dim() == 2, "top_index must be 2-D [rows, k]")
+    k = int(top_index.shape[1])
+    _require(1 <= k <= OPD_TOPK_MAX, f"k must be in [1, {OPD_TOPK_MAX}], got {k}")
+    _rows_matrix(top_index, "top_index", rows, k, torch.int32)
+    _rows_matrix(top_logit, "top_logit", rows, k, torch.float32)
+    _vector(rest_lse, "rest_lse", rows, torch.float32, optional=True)
+    _require(kl in OPD_KL, f"kl must be one of {sorted(OPD_KL)}, got {kl!r}")
+    args = (zp, dt, rows, vocab, ld, top_index.data_ptr(), top_logit.data_ptr(), k, _ptr(rest_lse), OPD_KL[kl],
+            float(alpha), float(tau))
+    lists = [("top_index", top_index), ("top_logit", top_logit), ("rest_lse", rest_lse)]
+    return args, rows, vocab, lists
+
+
+def _dz_arg(dz, z, rows, vocab):
+    """Checks a caller's dz against z."""
+    _dtype_code(dz)
+    _, rows_d, vocab_d, _ = _matrix(dz, "dz", whole_vectors=False)
+    _require((rows_d, vocab_d) == (rows, vocab), f"dz must be [{rows}, {vocab}], got {tuple(dz.shape)}")
+    _no_overlap(dz, z, "dz", "z")
+
+
+def topk_loss_fwd(z, top_index, top_logit, rest_lse, alpha: float, tau: float, kl: str = "reverse", scratch=None,
+                  ws=None):
+    """Distillation loss against a teacher's top logits (opd_topk_loss_fwd).
+
+    z [R, V]; top_index [R, k] int32 (negative: no entry), top_logit [R, k] f32 and rest_lse [R] f32
+    (None: the teacher's list is all of its distribution) as topk_rows gives them; kl "reverse" or
+    "forward". Returns (loss [R] f32, row_stats [R, 4] f32).
+    """
+    torch = _torch()
+    args, rows, vocab, lists = _topk_loss_args(z, top_index, top_logit, rest_lse, alpha, tau, kl)
+    _require(scratch is None or scratch.is_contiguous(), "scratch must be contiguous")
+    dev = z.device
+    _same_device(dev, lists + [("scratch", scratch)])
+    lib = load_library()
+    with _device_guard(dev):
+        ws = _workspace_arg(ws, dev)
+        scratch = _scratch_arg(scratch, lib.opd_topk_loss_scratch_size(rows, vocab, args[1]), dev)
+        loss = torch.empty(rows, dtype=torch.float32, device=dev)
+        stats = torch.empty(rows, 4, dtype=torch.float32, device=dev)
+        st = lib.opd_topk_loss_fwd(*args, loss.data_ptr(), stats.data_ptr(), _ptr(scratch), _nbytes(scratch),
+                                   ws.data_ptr(), ws.numel(), _stream(dev))
+    _check("opd_topk_loss_fwd", st)
+    return loss, stats
+
+
+def topk_loss_bwd(z, top_index, top_logit, rest_lse, alpha: float, tau: float, row_stats, kl: str = "reverse",
+                  grad_loss=None, dz_dtype=None, dz=None, ws=None):
+    """Returns dz [R, V] (dz_dtype, default z.dtype) = grad_loss[row] * d loss_row / d z_row, from the
+    row_stats of topk_loss_fwd on the same arguments (opd_topk_loss_bwd)."""
+    torch = _torch()
+    args, rows, vocab, lists = _topk_loss_args(z, top_index, top_logit, rest_lse, alpha, tau, kl)
+    _rows_matrix(row_stats, "row_stats", rows, 4, torch.float32)
+    _vector(grad_loss, "grad_loss", rows, torch.float32, optional=True)
+    if dz is not None:
+        _dz_arg(dz, z, rows, vocab)
+    dev = z.device
+    _same_device(dev, lists + [("row_stats", row_stats), ("grad_loss", grad_loss), ("dz", dz)])
+    lib = load_library()
+    with _device_guard(dev):
+        ws = _workspace_arg(ws, dev)
+        if dz is None:
+            dz = _empty_rows(rows, vocab, dz_dtype or z.dtype, dev)
+        dzp, _, _, ld_dz = _matrix(dz, "dz", whole_vectors=False)
+        st = lib.opd_topk_loss_bwd(*args, row_stats.data_ptr(), _ptr(grad_loss), dzp, _dtype_code(dz), ld_dz,
+                                   ws.data_ptr(), ws.numel(), _stream(dev))
+    _check("opd_topk_loss_bwd", st)
+    return dz
+
+
+def topk_fused_fwd_bwd(z, top_index, top_logit, rest_lse, alpha: float, tau: float, kl: str = "reverse",
+                       grad_loss=None, dz_dtype=None, scratch=None, out=None, ws=None) -> dict:
+    """topk_loss_fwd and topk_loss_bwd in one call (opd_topk_fused_fwd_bwd). Returns a dict of loss [R] f32,
+    row_stats [R, 4] f32 and dz [R, V]; ``out`` may hold preallocated tensors under the same keys."""
+    torch = _torch()
+    args, rows, vocab, lists = _topk_loss_args(z, top_index, top_logit, rest_lse, alpha, tau, kl)
+    _vector(grad_loss, "grad_loss", rows, torch.float32, optional=True)
+    _require(scratch is None or scratch.is_contiguous(), "scratch must be contiguous")
+    o = dict(out) if out is not None else {}
+    if o:
+        _vector(o.get("loss"), "loss", rows, torch.float32)
+        _require(o.get("row_stats") is not None, "out['row_stats'] is missing")
+        _rows_matrix(o["row_stats"], "row_stats", rows, 4, torch.float32)
+        _require(o.get("dz") is not None, "out['dz'] is missing")
+        _dz_arg(o["dz"], z, rows, vocab)
+    dev = z.device
+    _same_device(dev, lists + [("grad_loss", grad_loss), ("scratch", scratch)]
+                 + [(n, o.get(n)) for n in ("loss", "row_stats", "dz")])
+    lib = load_library()
+    with _device_guard(dev):
+        ws = _workspace_arg(ws, dev)
+        scratch = _scratch_arg(scratch, lib.opd_topk_loss_scratch_size(rows, vocab, args[1]), dev)
+        if not o:
+            o["loss"] = torch.empty(rows, dtype=torch.float32, device=dev)
+            o["row_stats"] = torch.empty(rows, 4, dtype=torch.float32, device=dev)
+            o["dz"] = _empty_rows(rows, vocab, dz_dtype or z.dtype, dev)
+        dzp, _, _, ld_dz = _matrix(o["dz"], "dz", whole_vectors=False)
+        st = lib.opd_topk_fused_fwd_bwd(*args, _ptr(grad_loss), o["loss"].data_ptr(), o["row_stats"].data_ptr(), dzp,
+                                        _dtype_code(o["dz"]), ld_dz, _ptr(scratch), _nbytes(scratch), ws.data_ptr(),
+                                        ws.numel(), _stream(dev))
+    _check("opd_topk_fused_fwd_bwd", st)
+    return o

@@ -23,6 +23,8 @@ static_assert(OPD_FLAG_NEG_L == opd::kFlagNegL, "flag mismatch");
 static_assert(OPD_FLAG_BAD_OFFSETS == opd::kFlagBadOffsets, "flag mismatch");
 static_assert(OPD_FLAG_SPIN_TIMEOUT == opd::kFlagSpinTimeout, "flag mismatch");
 static_assert(OPD_FLAG_BAD_TOKEN == opd::kFlagBadToken, "flag mismatch");
+static_assert(OPD_FLAG_BAD_LIST == opd::kFlagBadList, "flag mismatch");
+static_assert(OPD_FLAG_EMPTY_MASK == opd::kFlagEmptyMask, "flag mismatch");
 
 namespace {
 
@@ -84,12 +86,14 @@ opd_status_t check_ws(void* ws, size_t ws_bytes) {
   return OPD_OK;
 }
 
-opd_status_t check_dz(const void* dz, opd_dtype_t dz_dt, int64_t n_rows, int64_t vocab, int64_t ld_dz) {
-  if (n_rows > 0 && !dz) return fail(OPD_ERR_NULL, "dz must be non-NULL");
-  if (!valid_dtype(dz_dt)) return fail(OPD_ERR_DTYPE, "dz dtype must be OPD_F32 or OPD_BF16");
-  if (ld_dz < vocab) return fail(OPD_ERR_SHAPE, "ld_dz must be >= vocab");
-  if (!aligned16(dz)) return fail(OPD_ERR_ALIGN, "dz must be 16-byte aligned");
-  if ((ld_dz * (int64_t)dtype_size(dz_dt)) % 16 != 0) return fail(OPD_ERR_ALIGN, "dz row pitch must be a multiple of 16 bytes");
+opd_status_t check_dz(const void* dz, opd_dtype_t dz_dt, int64_t n_rows, int64_t vocab, int64_t ld_dz,
+                      const std::string& name = "dz") {
+  if (n_rows > 0 && !dz) return fail(OPD_ERR_NULL, name + " must be non-NULL");
+  if (!valid_dtype(dz_dt)) return fail(OPD_ERR_DTYPE, name + " dtype must be OPD_F32 or OPD_BF16");
+  if (ld_dz < vocab) return fail(OPD_ERR_SHAPE, "ld_" + name + " must be >= vocab");
+  if (!aligned16(dz)) return fail(OPD_ERR_ALIGN, name + " must be 16-byte aligned");
+  if ((ld_dz * (int64_t)dtype_size(dz_dt)) % 16 != 0)
+    return fail(OPD_ERR_ALIGN, name + " row pitch must be a multiple of 16 bytes");
   return OPD_OK;
 }
 
@@ -226,6 +230,8 @@ std::string flag_text(uint32_t f) {
   if (f & OPD_FLAG_BAD_OFFSETS) t += " malformed offsets;";
   if (f & OPD_FLAG_SPIN_TIMEOUT) t += " cross-workgroup wait timed out (outputs invalid);";
   if (f & OPD_FLAG_BAD_TOKEN) t += " proposal outside the vocabulary;";
+  if (f & OPD_FLAG_BAD_LIST) t += " list length, mask number or repeated token;";
+  if (f & OPD_FLAG_EMPTY_MASK) t += " mask without an allowed token;";
   return t;
 }
 
@@ -614,6 +620,225 @@ static opd_status_t opd_lmhead_fused_fwd_bwd_verify_impl(const void* h, const vo
   return run_accept(blocks, n_rows, draft_top1, target_top1, accept_len, ws, stream);
 }
 
+static int vectors_per_row(int64_t vocab, opd_dtype_t dt) {
+  const int epv = dt == OPD_BF16 ? 8 : 4;
+  return (int)((vocab + epv - 1) / epv);
+}
+
+static opd_status_t opd_adjust_logits_impl(const void* x, opd_dtype_t dt, int64_t n_rows, int64_t vocab, int64_t ld,
+                                           const opd_adjust_t* a, void* out, int64_t ld_out, void* ws,
+                                           size_t ws_bytes, hipStream_t stream) {
+  opd_status_t s = check_logits(x, x, dt, n_rows, vocab, ld);
+  if (s != OPD_OK) return s;
+  if ((s = check_dz(out, dt, n_rows, vocab, ld_out, "out")) != OPD_OK) return s;
+  if (!a) return fail(OPD_ERR_NULL, "adjust must be non-NULL");
+  if (a->n_blocks < 0) return fail(OPD_ERR_SHAPE, "n_blocks must be >= 0");
+  if (a->n_blocks > 0 && !a->offsets) return fail(OPD_ERR_NULL, "offsets must be non-NULL");
+  if (a->history) {
+    if (a->max_history < 0 || a->ld_history < a->max_history)
+      return fail(OPD_ERR_SHAPE, "ld_history must be >= max_history >= 0");
+    if (a->n_blocks > 0 && !a->history_len) return fail(OPD_ERR_NULL, "history needs history_len");
+  }
+  if (a->bias_tokens || a->bias_values) {
+    if (!a->bias_tokens || !a->bias_values || !a->bias_len)
+      return fail(OPD_ERR_NULL, "bias_tokens, bias_values and bias_len go together");
+    if (a->max_bias < 0 || a->max_bias > opd::kMaxBias || a->ld_bias < a->max_bias)
+      return fail(OPD_ERR_SHAPE, "max_bias must be in [0, 16384] and ld_bias >= max_bias");
+  }
+  if (a->mask) {
+    if (a->ld_mask < (vocab + 31) / 32) return fail(OPD_ERR_SHAPE, "ld_mask must be >= ceil(vocab / 32)");
+    if (a->n_masks < 0 || (!a->mask_row && a->n_masks < n_rows))
+      return fail(OPD_ERR_SHAPE, "one mask per row is needed without mask_row");
+    if (std::isnan(a->masked_value)) return fail(OPD_ERR_PARAM, "masked_value must not be NaN");
+  }
+  if (x == out && ld != ld_out) return fail(OPD_ERR_SHAPE, "in place, ld and ld_out must be equal");
+  if ((s = check_ws(ws, ws_bytes)) != OPD_OK) return s;
+  if (n_rows == 0 || a->n_blocks == 0) return OPD_OK;
+  opd::AdjustParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = static_cast<const uint8_t*>(x);
+  p.out = static_cast<uint8_t*>(out);
+  p.ld_bytes = ld * (int64_t)dtype_size(dt);
+  p.ld_out_bytes = ld_out * (int64_t)dtype_size(dt);
+  p.vocab = (int32_t)vocab;
+  p.nvec = vectors_per_row(vocab, dt);
+  p.n_rows = (int32_t)n_rows;
+  p.n_blocks = a->n_blocks;
+  p.offsets = a->offsets;
+  p.draft = a->draft_tokens;
+  p.history = a->history;
+  p.ld_history = a->ld_history;
+  p.max_history = a->max_history;
+  p.history_len = a->history_len;
+  p.prompt_len = a->prompt_len;
+  p.repetition = a->repetition;
+  p.frequency = a->frequency;
+  p.presence = a->presence;
+  p.bias_tokens = a->bias_tokens;
+  p.bias_values = a->bias_values;
+  p.ld_bias = a->ld_bias;
+  p.max_bias = a->max_bias;
+  p.bias_len = a->bias_len;
+  p.mask = reinterpret_cast<const uint8_t*>(a->mask);
+  p.ld_mask_bytes = a->ld_mask * 4;
+  p.n_masks = a->n_masks;
+  p.mask_row = a->mask_row;
+  p.masked_value = a->masked_value;
+  p.flags = static_cast<uint32_t*>(ws);
+  hipError_t e = opd::launch_adjust(p, dt == OPD_BF16, stream);
+  if (e != hipSuccess) return hip_fail(e, "adjust kernel launch");
+  return OPD_OK;
+}
+
+static opd_status_t check_scratch(const void* scratch, size_t bytes, size_t need, const char* what) {
+  if (need == 0) return OPD_OK;
+  if (!scratch || bytes < need) return fail(OPD_ERR_WORKSPACE, std::string("scratch missing or smaller than ") + what);
+  if (!aligned16(scratch)) return fail(OPD_ERR_ALIGN, "scratch must be 16-byte aligned");
+  return OPD_OK;
+}
+
+size_t opd_topk_scratch_size(int64_t n_rows, int64_t vocab, opd_dtype_t dt, int32_t k) {
+  if (n_rows <= 0 || n_rows > INT32_MAX || vocab <= 0 || vocab > kMaxVocab || !valid_dtype(dt) || k < 1 ||
+      k > opd::kTopkMax)
+    return 0;
+  int32_t seg = 1, seg_vec = 0;
+  opd::topk_split(n_rows, vectors_per_row(vocab, dt), k, &seg, &seg_vec);
+  return seg == 1 ? 0 : (size_t)n_rows * seg * (8 * (size_t)k + 8);
+}
+
+static opd_status_t opd_topk_rows_impl(const void* y, opd_dtype_t dt, int64_t n_rows, int64_t vocab, int64_t ld,
+                                       int32_t k, float* values, int32_t* index, float* rest_lse, void* scratch,
+                                       size_t scratch_bytes, void* ws, size_t ws_bytes, hipStream_t stream) {
+  opd_status_t s = check_logits(y, y, dt, n_rows, vocab, ld);
+  if (s != OPD_OK) return s;
+  if (k < 1 || k > opd::kTopkMax || k > vocab) return fail(OPD_ERR_SHAPE, "k must be in [1, min(256, vocab)]");
+  if (n_rows > 0 && (!values || !index || !rest_lse))
+    return fail(OPD_ERR_NULL, "values, index and rest_lse must be non-NULL");
+  if ((s = check_scratch(scratch, scratch_bytes, opd_topk_scratch_size(n_rows, vocab, dt, k),
+                         "opd_topk_scratch_size()")) != OPD_OK)
+    return s;
+  if ((s = check_ws(ws, ws_bytes)) != OPD_OK) return s;
+  if (n_rows == 0) return OPD_OK;
+  opd::TopkParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.y = static_cast<const uint8_t*>(y);
+  p.ld_bytes = ld * (int64_t)dtype_size(dt);
+  p.vocab = (int32_t)vocab;
+  p.nvec = vectors_per_row(vocab, dt);
+  p.n_rows = (int32_t)n_rows;
+  p.k = k;
+  opd::topk_split(n_rows, p.nvec, k, &p.n_seg, &p.seg_vec);
+  p.values = values;
+  p.index = index;
+  p.rest_lse = rest_lse;
+  if (p.n_seg > 1) {
+    p.seg_keys = static_cast<uint64_t*>(scratch);
+    p.seg_lse = reinterpret_cast<float*>(p.seg_keys + (size_t)n_rows * p.n_seg * k);
+  }
+  hipError_t e = opd::launch_topk(p, dt == OPD_BF16, stream);
+  if (e != hipSuccess) return hip_fail(e, "top-k kernel launch");
+  return OPD_OK;
+}
+
+size_t opd_topk_loss_scratch_size(int64_t n_rows, int64_t vocab, opd_dtype_t dt) {
+  if (n_rows <= 0 || n_rows > INT32_MAX || vocab <= 0 || vocab > kMaxVocab || !valid_dtype(dt)) return 0;
+  int32_t seg = 1, seg_vec = 0;
+  opd::topk_loss_split(n_rows, vectors_per_row(vocab, dt), &seg, &seg_vec);
+  return (size_t)n_rows * seg * 8;
+}
+
+// Checks of the arguments that the three calls share, and the parameters that go with them.
+static opd_status_t topk_loss_params(const void* z, opd_dtype_t dt, int64_t n_rows, int64_t vocab, int64_t ld,
+                                     const int32_t* top_index, const float* top_logit, int32_t k,
+                                     const float* rest_lse, opd_kl_t kl, float alpha, float tau, void* ws,
+                                     size_t ws_bytes, opd::TopkLossParams* p) {
+  opd_status_t s = check_logits(z, z, dt, n_rows, vocab, ld);
+  if (s != OPD_OK) return s;
+  if (k < 1 || k > opd::kTopkMax) return fail(OPD_ERR_SHAPE, "k must be in [1, 256]");
+  if (n_rows > 0 && (!top_index || !top_logit)) return fail(OPD_ERR_NULL, "top_index and top_logit must be non-NULL");
+  if ((s = check_params(alpha, tau)) != OPD_OK) return s;
+  if (kl != OPD_KL_REVERSE && kl != OPD_KL_FORWARD)
+    return fail(OPD_ERR_PARAM, "kl must be OPD_KL_REVERSE or OPD_KL_FORWARD");
+  if (kl == OPD_KL_REVERSE && !rest_lse && tau > 0.f && std::isinf(tau))
+    return fail(OPD_ERR_PARAM, "the reverse divergence without rest_lse needs a finite tau");
+  if ((s = check_ws(ws, ws_bytes)) != OPD_OK) return s;
+  std::memset(p, 0, sizeof(*p));
+  p->z = static_cast<const uint8_t*>(z);
+  p->ld_bytes = ld * (int64_t)dtype_size(dt);
+  p->vocab = (int32_t)vocab;
+  p->nvec = vectors_per_row(vocab, dt);
+  p->n_rows = (int32_t)n_rows;
+  p->k = k;
+  p->top_index = top_index;
+  p->top_logit = top_logit;
+  p->rest_lse = rest_lse;
+  p->kl = kl;
+  p->alpha = alpha;
+  p->tau = tau;
+  p->flags = static_cast<uint32_t*>(ws);
+  opd::topk_loss_split(n_rows, p->nvec, &p->n_seg, &p->seg_vec);
+  return OPD_OK;
+}
+
+static opd_status_t opd_topk_loss_fwd_impl(const void* z, opd_dtype_t dt, int64_t n_rows, int64_t vocab, int64_t ld,
+                                           const int32_t* top_index, const float* top_logit, int32_t k,
+                                           const float* rest_lse, opd_kl_t kl, float alpha, float tau, float* loss,
+                                           float* row_stats, void* scratch, size_t scratch_bytes, void* ws,
+                                           size_t ws_bytes, hipStream_t stream) {
+  opd::TopkLossParams p;
+  opd_status_t s = topk_loss_params(z, dt, n_rows, vocab, ld, top_index, top_logit, k, rest_lse, kl, alpha, tau, ws,
+                                    ws_bytes, &p);
+  if (s != OPD_OK) return s;
+  if (n_rows > 0 && (!loss || !row_stats)) return fail(OPD_ERR_NULL, "loss and row_stats must be non-NULL");
+  if ((s = check_scratch(scratch, scratch_bytes, opd_topk_loss_scratch_size(n_rows, vocab, dt),
+                         "opd_topk_loss_scratch_size()")) != OPD_OK)
+    return s;
+  if (n_rows == 0) return OPD_OK;
+  p.loss = loss;
+  p.row_stats = row_stats;
+  p.seg_lse = static_cast<float*>(scratch);
+  hipError_t e = opd::launch_topk_loss_fwd(p, dt == OPD_BF16, stream);
+  if (e != hipSuccess) return hip_fail(e, "top-k loss kernel launch");
+  return OPD_OK;
+}
+
+static opd_status_t opd_topk_loss_bwd_impl(const void* z, opd_dtype_t dt, int64_t n_rows, int64_t vocab, int64_t ld,
+                                           const int32_t* top_index, const float* top_logit, int32_t k,
+                                           const float* rest_lse, opd_kl_t kl, float alpha, float tau,
+                                           const float* row_stats, const float* grad_loss, void* dz,
+                                           opd_dtype_t dz_dt, int64_t ld_dz, void* ws, size_t ws_bytes,
+                                           hipStream_t stream) {
+  opd::TopkLossParams p;
+  opd_status_t s = topk_loss_params(z, dt, n_rows, vocab, ld, top_index, top_logit, k, rest_lse, kl, alpha, tau, ws,
+                                    ws_bytes, &p);
+  if (s != OPD_OK) return s;
+  if (n_rows > 0 && !row_stats) return fail(OPD_ERR_NULL, "row_stats must be non-NULL");
+  if ((s = check_dz(dz, dz_dt, n_rows, vocab, ld_dz)) != OPD_OK) return s;
+  if (n_rows == 0) return OPD_OK;
+  p.row_stats = const_cast<float*>(row_stats);  // (read only by this call's kernel)
+  p.grad_loss = grad_loss;
+  p.dz = static_cast<uint8_t*>(dz);
+  p.ld_dz_bytes = ld_dz * (int64_t)dtype_size(dz_dt);
+  hipError_t e = opd::launch_topk_loss_bwd(p, dt == OPD_BF16, dz_dt == OPD_BF16, stream);
+  if (e != hipSuccess) return hip_fail(e, "top-k loss gradient kernel launch");
+  return OPD_OK;
+}
+
+static opd_status_t opd_topk_fused_fwd_bwd_impl(const void* z, opd_dtype_t dt, int64_t n_rows, int64_t vocab,
+                                                int64_t ld, const int32_t* top_index, const float* top_logit,
+                                                int32_t k, const float* rest_lse, opd_kl_t kl, float alpha, float tau,
+                                                const float* grad_loss, float* loss, float* row_stats, void* dz,
+                                                opd_dtype_t dz_dt, int64_t ld_dz, void* scratch, size_t scratch_bytes,
+                                                void* ws, size_t ws_bytes, hipStream_t stream) {
+  opd_status_t s = check_dz(dz, dz_dt, n_rows, vocab, ld_dz);
+  if (s != OPD_OK) return s;
+  s = opd_topk_loss_fwd_impl(z, dt, n_rows, vocab, ld, top_index, top_logit, k, rest_lse, kl, alpha, tau, loss,
+                             row_stats, scratch, scratch_bytes, ws, ws_bytes, stream);
+  if (s != OPD_OK) return s;
+  return opd_topk_loss_bwd_impl(z, dt, n_rows, vocab, ld, top_index, top_logit, k, rest_lse, kl, alpha, tau,
+                                row_stats, grad_loss, dz, dz_dt, ld_dz, ws, ws_bytes, stream);
+}
+
 opd_status_t opd_read_flags(void* ws, size_t ws_bytes, int clear, uint32_t* flags, hipStream_t stream) {
   if (!flags) return fail(OPD_ERR_NULL, "flags must be non-NULL");
   opd_status_t s = check_ws(ws, ws_bytes);
@@ -714,6 +939,52 @@ opd_status_t opd_lmhead_fused_fwd_bwd_verify(const void* h, const void* W, int64
                                                      grad_loss, loss, target_top1, draft_top1, row_stats, dh, dW,
                                                      logit_max_lse, logit_argmax, accept_len, scratch, scratch_bytes,
                                                      chunk_rows, ws, ws_bytes, stream),
+                ws, stream);
+}
+
+opd_status_t opd_adjust_logits(const void* x, opd_dtype_t dt, int64_t n_rows, int64_t vocab, int64_t ld,
+                               const opd_adjust_t* adjust, void* out, int64_t ld_out, void* ws, size_t ws_bytes,
+                               hipStream_t stream) {
+  return finish(opd_adjust_logits_impl(x, dt, n_rows, vocab, ld, adjust, out, ld_out, ws, ws_bytes, stream), ws,
+                stream);
+}
+
+opd_status_t opd_topk_rows(const void* y, opd_dtype_t dt, int64_t n_rows, int64_t vocab, int64_t ld, int32_t k,
+                           float* values, int32_t* index, float* rest_lse, void* scratch, size_t scratch_bytes,
+                           void* ws, size_t ws_bytes, hipStream_t stream) {
+  return finish(opd_topk_rows_impl(y, dt, n_rows, vocab, ld, k, values, index, rest_lse, scratch, scratch_bytes, ws,
+                                   ws_bytes, stream),
+                ws, stream);
+}
+
+opd_status_t opd_topk_loss_fwd(const void* z, opd_dtype_t dt, int64_t n_rows, int64_t vocab, int64_t ld,
+                               const int32_t* top_index, const float* top_logit, int32_t k, const float* rest_lse,
+                               opd_kl_t kl, float alpha, float tau, float* loss, float* row_stats, void* scratch,
+                               size_t scratch_bytes, void* ws, size_t ws_bytes, hipStream_t stream) {
+  return finish(opd_topk_loss_fwd_impl(z, dt, n_rows, vocab, ld, top_index, top_logit, k, rest_lse, kl, alpha, tau,
+                                       loss, row_stats, scratch, scratch_bytes, ws, ws_bytes, stream),
+                ws, stream);
+}
+
+opd_status_t opd_topk_loss_bwd(const void* z, opd_dtype_t dt, int64_t n_rows, int64_t vocab, int64_t ld,
+                               const int32_t* top_index, const float* top_logit, int32_t k, const float* rest_lse,
+                               opd_kl_t kl, float alpha, float tau, const float* row_stats, const float* grad_loss,
+                               void* dz, opd_dtype_t dz_dt, int64_t ld_dz, void* ws, size_t ws_bytes,
+                               hipStream_t stream) {
+  return finish(opd_topk_loss_bwd_impl(z, dt, n_rows, vocab, ld, top_index, top_logit, k, rest_lse, kl, alpha, tau,
+                                       row_stats, grad_loss, dz, dz_dt, ld_dz, ws, ws_bytes, stream),
+                ws, stream);
+}
+
+opd_status_t opd_topk_fused_fwd_bwd(const void* z, opd_dtype_t dt, int64_t n_rows, int64_t vocab, int64_t ld,
+                                    const int32_t* top_index, const float* top_logit, int32_t k,
+                                    const float* rest_lse, opd_kl_t kl, float alpha, float tau,
+                                    const float* grad_loss, float* loss, float* row_stats, void* dz,
+                                    opd_dtype_t dz_dt, int64_t ld_dz, void* scratch, size_t scratch_bytes, void* ws,
+                                    size_t ws_bytes, hipStream_t stream) {
+  return finish(opd_topk_fused_fwd_bwd_impl(z, dt, n_rows, vocab, ld, top_index, top_logit, k, rest_lse, kl, alpha,
+                                            tau, grad_loss, loss, row_stats, dz, dz_dt, ld_dz, scratch, scratch_bytes,
+                                            ws, ws_bytes, stream),
                 ws, stream);
 }
 

@@ -33,6 +33,8 @@ constexpr uint32_t kFlagNegL = 1u;
 constexpr uint32_t kFlagBadOffsets = 2u;
 constexpr uint32_t kFlagSpinTimeout = 4u;
 constexpr uint32_t kFlagBadToken = 8u;
+constexpr uint32_t kFlagBadList = 16u;
+constexpr uint32_t kFlagEmptyMask = 32u;
 constexpr uint32_t kDefaultSpinLimit = 1u << 22;
 // A device epoch past this value is restarted at 0 by the last workgroup of a launch, which first
 // zeroes every exchange unit (no flag of the range that ends can then match a stale unit).
@@ -138,6 +140,84 @@ struct SampleParams {
   int32_t block0;  // first block of the current batch
 };
 
+// Penalties, biases and masks on the rows of packed blocks (opd_adjust.hip).
+constexpr int kMaxBias = 16384;  // entries of one request's bias list
+struct AdjustParams {
+  const uint8_t* x;
+  uint8_t* out;
+  int64_t ld_bytes;
+  int64_t ld_out_bytes;
+  int32_t vocab;
+  int32_t nvec;  // 16-byte vectors per row covering vocab
+  int32_t n_rows;
+  int32_t n_blocks;
+  const int32_t* offsets;
+  const int32_t* draft;  // nullable, as every list below
+  const int32_t* history;
+  int64_t ld_history;
+  int32_t max_history;
+  const int32_t* history_len;
+  const int32_t* prompt_len;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int32_t* bias_tokens;
+  const float* bias_values;
+  int64_t ld_bias;
+  int32_t max_bias;
+  const int32_t* bias_len;
+  const uint8_t* mask;
+  int64_t ld_mask_bytes;
+  int32_t n_masks;
+  const int32_t* mask_row;
+  float masked_value;
+  uint32_t* flags;
+};
+
+// A row's k largest logits and the log-sum-exp of the others (opd_topk.hip).
+constexpr int kTopkMax = OPD_TOPK_MAX;
+constexpr int kTopkCap = 4096;  // candidate keys a workgroup holds in LDS
+struct TopkParams {
+  const uint8_t* y;
+  int64_t ld_bytes;
+  int32_t vocab;
+  int32_t nvec;
+  int32_t n_rows;
+  int32_t k;
+  int32_t n_seg;    // segments a row is split into, each selected by a workgroup of its own
+  int32_t seg_vec;  // vectors per segment
+  float* values;
+  int32_t* index;
+  float* rest_lse;
+  uint64_t* seg_keys;  // scratch [n_rows][n_seg][k], largest first (n_seg > 1)
+  float* seg_lse;      // scratch [n_rows][n_seg][2]: reference and sum of the segment's other logits
+};
+
+// Distillation from a teacher's top logits (opd_topk_loss.hip).
+struct TopkLossParams {
+  const uint8_t* z;
+  int64_t ld_bytes;
+  int32_t vocab;
+  int32_t nvec;
+  int32_t n_rows;
+  int32_t k;
+  const int32_t* top_index;
+  const float* top_logit;
+  const float* rest_lse;  // nullable
+  int32_t kl;
+  float alpha;
+  float tau;
+  const float* grad_loss;  // nullable
+  float* loss;
+  float* row_stats;  // [n_rows][4]
+  uint8_t* dz;
+  int64_t ld_dz_bytes;
+  int32_t n_seg;
+  int32_t seg_vec;
+  float* seg_lse;  // scratch [n_rows][n_seg][2]
+  uint32_t* flags;
+};
+
 // in_bf16: 1 if z/y are bf16 (else fp32); out_bf16: 1 if dz is bf16 (else fp32); K: slots per thread
 // (1, 3 or 5).
 hipError_t launch_team(const TeamParams& p, int mode, int in_bf16, int out_bf16, int K, int grid,
@@ -150,6 +230,13 @@ hipError_t launch_fill_u32(uint32_t* dst, uint32_t value, size_t count, hipStrea
 hipError_t launch_stream_probe(const void* a, const void* b, void* c, size_t n_vec, hipStream_t s);
 hipError_t launch_length_head(const LengthHeadParams& p, hipStream_t s);  // opd_epilogue.hip
 hipError_t launch_sample_verify(const SampleParams& p, int in_bf16, hipStream_t s);  // opd_sample.hip
+hipError_t launch_adjust(const AdjustParams& p, int in_bf16, hipStream_t s);  // opd_adjust.hip
+// Segments a row is split into, and vectors per segment; both sizes in 16-byte vectors.
+void topk_split(int64_t n_rows, int32_t nvec, int32_t k, int32_t* n_seg, int32_t* seg_vec);
+hipError_t launch_topk(const TopkParams& p, int in_bf16, hipStream_t s);  // opd_topk.hip
+void topk_loss_split(int64_t n_rows, int32_t nvec, int32_t* n_seg, int32_t* seg_vec);
+hipError_t launch_topk_loss_fwd(const TopkLossParams& p, int in_bf16, hipStream_t s);  // opd_topk_loss.hip
+hipError_t launch_topk_loss_bwd(const TopkLossParams& p, int in_bf16, int out_bf16, hipStream_t s);
 
 // Records the detail text returned by opd_last_error() on this thread (opd_api.cpp).
 opd_status_t record_error(opd_status_t s, const char* msg);

@@ -80,7 +80,11 @@ typedef enum {
 #define OPD_FLAG_NEG_L 1u        /* some block had L < 0 (treated as 0)                         */
 #define OPD_FLAG_BAD_OFFSETS 2u  /* some block had decreasing / out-of-range offsets (accept 0)   */
 #define OPD_FLAG_SPIN_TIMEOUT 4u /* a cross-workgroup wait exceeded its bound: outputs invalid    */
-#define OPD_FLAG_BAD_TOKEN 8u    /* a verified row proposed a token outside [0, vocab) (rejected)  */
+#define OPD_FLAG_BAD_TOKEN 8u    /* a verified row proposed a token outside [0, vocab) (rejected); or
+                                    a token list (history, bias, teacher's top) names one (ignored)  */
+#define OPD_FLAG_BAD_LIST 16u    /* a list's length or a mask row's number was out of range (clamped /
+                                    no mask), or a teacher's list names a token twice (first counts)  */
+#define OPD_FLAG_EMPTY_MASK 32u  /* a row's grammar mask allows no token                              */
 
 /* Packed verification blocks ("Infrastructure: ... Variable-Length Batching"): block b owns rows
  * offsets[b] .. offsets[b+1]-1; L[b] is the length head's predicted verification length.
@@ -273,6 +277,144 @@ opd_status_t opd_lmhead_fused_fwd_bwd_verify(const void* h, const void* W, int64
                                              float* logit_max_lse, int32_t* logit_argmax, int32_t* accept_len,
                                              void* scratch, size_t scratch_bytes, int64_t chunk_rows, void* ws,
                                              size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Penalties for repeated tokens, biases and grammar masks on the logits of packed draft blocks, before
+ * they are verified ("2. Adaptive Length Head ...": blocks of drafted positions; "Infrastructure: ...
+ * Variable-Length Batching": packed by offsets). The pages name no such step; a server that offers
+ * its requests these settings needs it between the models' logits and opd_verify_sample /
+ * verify_accept_len, on the target's rows and (for speculative sampling to stay efficient) on the
+ * drafter's.
+ * Row j of block b continues request b's history by the proposals of the block's rows 0 .. j-1. With
+ * c_v = how often token v occurs in the request's output (history[prompt_len ..] and those proposals),
+ * known_v = whether v occurs in the prompt or the output, per element
+ *   x1 = known_v ? (x > 0 ? x / repetition : x * repetition) : x
+ *   x2 = x1 - frequency * c_v - presence * [c_v > 0] + bias_v
+ *   out = (the row has a mask and its bit v is 0) ? masked_value : x2
+ * in fp32, rounded once to the logits' type. Rows of a k-row block are independent calls of the same
+ * rule, so the last accepted row's distribution is the one that step-by-step decoding would have had.
+ * The struct lives on the host, its arrays on the device; every list is optional.
+ *   offsets          [n_blocks + 1] rows of each request, as in opd_blocks_t.
+ *   draft_tokens     [n_rows] proposal of each row, or NULL (rows do not see the block's earlier ones).
+ *   history          [n_blocks][ld_history] token of each request, history_len[b] of them (clamped to
+ *                    max_history), the first prompt_len[b] being the prompt (NULL: 0, all output);
+ *                    NULL: no history.
+ *   repetition, frequency, presence  [n_blocks] f32, each NULL for none (1, 0, 0); repetition > 0.
+ *   bias_tokens, bias_values  [n_blocks][ld_bias] tokens and f32 values, bias_len[b] of them (clamped
+ *                    to max_bias <= 16384); the last entry of a token listed twice counts; NULL: none.
+ *   mask             [n_masks][ld_mask] 32-bit words, token v allowed where bit v % 32 of word v / 32 is
+ *                    set (ld_mask >= ceil(vocab / 32)); mask_row [n_rows]: each row's mask or a negative
+ *                    number for none (NULL: row r has mask r, n_masks >= n_rows). mask NULL: none.
+ *   masked_value     what a masked logit becomes; -inf for a softmax of the caller's own; the row
+ *                    kernels of this library take logits of at most 1e4, so -1e4 before them. Not NaN.
+ * Tokens outside [0, vocab) are ignored (OPD_FLAG_BAD_TOKEN); a row whose mask allows nothing is
+ * masked_value everywhere (OPD_FLAG_EMPTY_MASK).
+ */
+typedef struct {
+  const int32_t* offsets;
+  int32_t n_blocks;
+  const int32_t* draft_tokens;
+  const int32_t* history;
+  int64_t ld_history;
+  int32_t max_history;
+  const int32_t* history_len;
+  const int32_t* prompt_len;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int32_t* bias_tokens;
+  const float* bias_values;
+  int64_t ld_bias;
+  int32_t max_bias;
+  const int32_t* bias_len;
+  const uint32_t* mask;
+  int64_t ld_mask;
+  int32_t n_masks;
+  const int32_t* mask_row;
+  float masked_value;
+} opd_adjust_t;
+
+/*
+ *   x       [n_rows, ld] logits of dtype dt; out [n_rows, ld_out] of the same dtype: x itself with the
+ *           same pitch (in place) or memory that does not overlap it.
+ * Logits may be infinite or NaN: an unmasked NaN stays NaN, a masked one becomes masked_value. Rows
+ * outside every block (and the pad of every row) are left as they are. No request needs more than one
+ * pass over its rows: each logit is read once and written once.
+ * Errors: OPD_ERR_NULL, OPD_ERR_SHAPE, OPD_ERR_DTYPE, OPD_ERR_ALIGN, OPD_ERR_PARAM (masked_value NaN),
+ * OPD_ERR_WORKSPACE, OPD_ERR_HIP.
+ */
+opd_status_t opd_adjust_logits(const void* x, opd_dtype_t dt, int64_t n_rows, int64_t vocab, int64_t ld,
+                               const opd_adjust_t* adjust, void* out, int64_t ld_out, void* ws,
+                               size_t ws_bytes, hipStream_t stream);
+
+/*
+ * The k largest logits of every row, and the log-sum-exp of all its others: what is kept of a target
+ * row for training later ("Infrastructure: Async Training ...": training runs apart from serving; a
+ * whole row of 151,936 bf16 logits is 304 KB, its top 64 with the rest 0.5 KB).
+ *   y         [n_rows, ld] logits of dtype dt; -inf allowed (a masked token), +inf and NaN not (numbers
+ *             unspecified; indices stay in [-1, vocab)).
+ *   k         1 .. min(OPD_TOPK_MAX, vocab).
+ *   values    [n_rows][k] f32 out, falling; index [n_rows][k] int32 out: equal logits by rising index.
+ *   rest_lse  [n_rows] f32 out: log sum over the tokens not listed of e^y, -inf if none has weight.
+ *   scratch   device memory of at least opd_topk_scratch_size(n_rows, vocab, dt, k) bytes (may be 0),
+ *             16-byte aligned; not shared by calls that run at once.
+ * Errors: OPD_ERR_NULL, OPD_ERR_SHAPE (k too), OPD_ERR_DTYPE, OPD_ERR_ALIGN, OPD_ERR_WORKSPACE,
+ * OPD_ERR_HIP.
+ */
+#define OPD_TOPK_MAX 256
+size_t opd_topk_scratch_size(int64_t n_rows, int64_t vocab, opd_dtype_t dt, int32_t k);
+opd_status_t opd_topk_rows(const void* y, opd_dtype_t dt, int64_t n_rows, int64_t vocab, int64_t ld, int32_t k,
+                           float* values, int32_t* index, float* rest_lse, void* scratch, size_t scratch_bytes,
+                           void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Distillation from a teacher's top logits: the loss of opd_loss_fwd where only k logits of each target
+ * row and the log-sum-exp of the others are at hand (opd_topk_rows; the pages: reverse KL with every
+ * term clipped before the sum, plus the target's top-1 as a hard label). The classes c of a row are its
+ * listed tokens and, as one class, all the others; p_c = the drafter's softmax(z) summed over class c,
+ * q = softmax(top_logit_1, .., top_logit_k, rest_lse):
+ *   OPD_KL_REVERSE  term_c = p_c (log p_c - log q_c)
+ *   OPD_KL_FORWARD  term_c = q_c (log q_c - log p_c)
+ *   loss = alpha * sum_c min(term_c, tau) + (1 - alpha) * (-log p_a),   a = the listed token of the
+ *          largest top_logit (lowest index on ties)
+ *   dz   = grad_loss[row] * d loss / d z; a clipped term has no gradient (term == tau passes, as for the
+ *          whole-row loss; an infinite term is clipped for any tau); none to the teacher's side.
+ *   z          [n_rows, ld] drafter logits of dtype dt, -inf allowed where a row keeps a finite one.
+ *   top_index, top_logit  [n_rows][k] int32 / f32, k = 1 .. OPD_TOPK_MAX, any order. A negative index is
+ *              an entry that is not there (shorter lists are padded with -1); one of vocab or more is
+ *              ignored (OPD_FLAG_BAD_TOKEN); of a token listed twice the first counts
+ *              (OPD_FLAG_BAD_LIST). -inf logits allowed (probability 0). A row with no entry of finite
+ *              logit takes no part: loss 0, dz 0.
+ *   rest_lse   [n_rows] f32, -inf allowed; NULL: -inf for every row (the teacher's list is all of it),
+ *              which the reverse divergence takes only with a finite tau.
+ *   loss       [n_rows] f32 out; row_stats [n_rows][4] f32 out, for the backward call: (reference and
+ *              log2 of the sum of 2^(z log2(e)) over the tokens not listed, log-sum-exp of the whole
+ *              row, divergence).
+ *   dz         [n_rows, ld_dz] of dtype dz_dt, every token's (up to vocab); must not overlap z.
+ *   scratch    device memory of at least opd_topk_loss_scratch_size(n_rows, vocab, dt) bytes (may be
+ *              0), 16-byte aligned; not shared by calls that run at once. The backward call needs none.
+ * The fused call gives the forward's and the backward's outputs, and z is read from HBM once where the
+ * rows' working set fits the chip. Separate and fused calls agree to rounding, not bit for bit.
+ * Errors: OPD_ERR_NULL, OPD_ERR_SHAPE (k too), OPD_ERR_DTYPE, OPD_ERR_ALIGN, OPD_ERR_PARAM (alpha, tau, kl),
+ * OPD_ERR_WORKSPACE, OPD_ERR_HIP.
+ */
+typedef enum { OPD_KL_REVERSE = 0, OPD_KL_FORWARD = 1 } opd_kl_t;
+size_t opd_topk_loss_scratch_size(int64_t n_rows, int64_t vocab, opd_dtype_t dt);
+opd_status_t opd_topk_loss_fwd(const void* z, opd_dtype_t dt, int64_t n_rows, int64_t vocab, int64_t ld,
+                               const int32_t* top_index, const float* top_logit, int32_t k, const float* rest_lse,
+                               opd_kl_t kl, float alpha, float tau, float* loss, float* row_stats, void* scratch,
+                               size_t scratch_bytes, void* ws, size_t ws_bytes, hipStream_t stream);
+opd_status_t opd_topk_loss_bwd(const void* z, opd_dtype_t dt, int64_t n_rows, int64_t vocab, int64_t ld,
+                               const int32_t* top_index, const float* top_logit, int32_t k, const float* rest_lse,
+                               opd_kl_t kl, float alpha, float tau, const float* row_stats, const float* grad_loss,
+                               void* dz, opd_dtype_t dz_dt, int64_t ld_dz, void* ws, size_t ws_bytes,
+                               hipStream_t stream);
+opd_status_t opd_topk_fused_fwd_bwd(const void* z, opd_dtype_t dt, int64_t n_rows, int64_t vocab, int64_t ld,
+                                    const int32_t* top_index, const float* top_logit, int32_t k,
+                                    const float* rest_lse, opd_kl_t kl, float alpha, float tau,
+                                    const float* grad_loss, float* loss, float* row_stats, void* dz,
+                                    opd_dtype_t dz_dt, int64_t ld_dz, void* scratch, size_t scratch_bytes, void* ws,
+                                    size_t ws_bytes, hipStream_t stream);
 
 /*
  * Host-side batch scheduling ("AdaFlash: Adaptive Speculative Decoding with Online Self-Improvement

@@ -1,0 +1,109 @@
+"""Float64 oracle of a row's top logits and of distillation against them (test infrastructure only; see
+opd_oracle for the rules of its use).
+
+A row's classes are its k listed tokens and, as one class, all the others (probability: the sum of
+theirs). With p the drafter's and q the teacher's distribution over the classes, the loss is the
+pages' (reverse KL with every term clipped before the sum, mixed with the target's top-1 as a hard
+label), over classes instead of tokens:
+
+    reverse  term_c = p_c (ln p_c - ln q_c)      forward  term_c = q_c (ln q_c - ln p_c)
+    loss = alpha sum_c min(term_c, tau) + (1 - alpha) (-ln p_a)
+
+and its gradient by the chain rule, term by term: d loss / d z_j = sum over classes of
+d loss / d p_c * d p_c / d z_j with d p_c / d z_j = p_c ([j in c] s_j - p_j), s_j = p_j / p_c.
+"""
+
+from __future__ import annotations
+
+import numpy as np
+
+__all__ = ["topk_row", "effective_list", "row_loss", "row_grad"]
+
+
+def lse(x) -> float:
+    x = np.asarray(x, dtype=np.float64)
+    if x.size == 0 or np.max(x) == -np.inf:
+        return -np.inf
+    m = float(np.max(x))
+    return m + float(np.log(np.sum(np.exp(x - m))))
+
+
+def topk_row(y, k: int):
+    """(values, indices, log-sum-exp of the others): falling values, equal ones by rising index."""
+    y = np.asarray(y, dtype=np.float64)
+    order = np.lexsort((np.arange(y.size), -y))
+    return y[order[:k]], order[:k], lse(y[order[k:]])
+
+
+def effective_list(index, vocab: int):
+    """Places in the list that count: not negative, below vocab, and the first of a token's."""
+    seen, keep = set(), []
+    for i, t in enumerate(int(t) for t in index):
+        if 0 <= t < vocab and t not in seen:
+            seen.add(t)
+            keep.append(i)
+    return keep
+
+
+def _classes(z, index, logit, rest_lse):
+    z = np.asarray(z, dtype=np.float64)
+    keep = effective_list(index, z.size)
+    tok = np.array([int(index[i]) for i in keep], dtype=np.int64)
+    t = np.array([float(logit[i]) for i in keep], dtype=np.float64)
+    others = np.ones(z.size, dtype=bool)
+    others[tok] = False
+    with np.errstate(divide="ignore"):
+        lp = np.append(z[tok], lse(z[others])) - lse(z)
+    lq = np.append(t, rest_lse)
+    lq = lq - lse(lq) if np.max(lq) > -np.inf else lq
+    return z, tok, t, others, lp, lq
+
+
+def _terms(lp, lq, kl):
+    p, q = np.exp(lp), np.exp(lq)
+    term = np.zeros_like(p)
+    w, lw, lo = (p, lp, lq) if kl == "reverse" else (q, lq, lp)
+    on = w > 0
+    term[on] = w[on] * (lw[on] - lo[on])
+    return term
+
+
+def row_loss(z, index, logit, rest_lse, alpha, tau, kl="reverse"):
+    """(loss, dict of the row's classes); a row with no entry of finite logit has loss 0."""
+    z, tok, t, others, lp, lq = _classes(z, index, logit, rest_lse)
+    info = dict(tok=tok, t=t, others=others, lp=lp, lq=lq, lse=lse(z), rest=lse(z[others]), active=False, div=0.0)
+    if t.size == 0 or np.max(t) == -np.inf:
+        return 0.0, info
+    term = _terms(lp, lq, kl)
+    div = float(np.sum(np.minimum(term, tau)))
+    a = int(np.min(tok[t == np.max(t)]))
+    place = int(np.flatnonzero(tok == a)[0])
+    loss = (alpha * div if alpha > 0 else 0.0) - ((1 - alpha) * lp[place] if alpha < 1 else 0.0)
+    info.update(term=term, div=div, a=a, place=place, active=True)
+    return float(loss), info
+
+
+def row_grad(z, index, logit, rest_lse, alpha, tau, kl="reverse"):
+    """(d loss / d z, info of row_loss)."""
+    _, info = row_loss(z, index, logit, rest_lse, alpha, tau, kl)
+    z = np.asarray(z, dtype=np.float64)
+    if not info["active"]:
+        return np.zeros_like(z), info
+    lp, lq, term = info["lp"], info["lq"], info["term"]
+    p, q = np.exp(lp), np.exp(lq)
+    through = (term <= tau) & np.isfinite(term)
+    # d loss / d p_c times p_c, so that a class of probability 0 needs no division
+    dp = np.zeros_like(p)
+    if kl == "reverse":
+        on = through & (p > 0)
+        dp[on] = alpha * p[on] * (lp[on] - lq[on] + 1.0)
+    else:
+        dp[through] = -alpha * q[through]
+    dp[info["place"]] -= 1.0 - alpha
+    pj = np.exp(z - info["lse"])
+    dz = -pj * dp.sum()
+    dz[info["tok"]] += dp[:-1]
+    if np.isfinite(info["rest"]):
+        o = info["others"]
+        dz[o] += np.exp(z[o] - info["rest"]) * dp[-1]
+    return dz, info
