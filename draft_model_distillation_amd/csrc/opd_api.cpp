@@ -742,9 +742,7 @@ static opd_status_t opd_topk_rows_impl(const void* y, opd_dtype_t dt, int64_t n_
 
 size_t opd_topk_loss_scratch_size(int64_t n_rows, int64_t vocab, opd_dtype_t dt) {
   if (n_rows <= 0 || n_rows > INT32_MAX || vocab <= 0 || vocab > kMaxVocab || !valid_dtype(dt)) return 0;
-  int32_t seg = 1, seg_vec = 0;
-  opd::topk_loss_split(n_rows, vectors_per_row(vocab, dt), &seg, &seg_vec);
-  return (size_t)n_rows * seg * 8;
+  return opd::topk_loss_scratch(n_rows, vectors_per_row(vocab, dt));
 }
 
 // Checks of the arguments that the three calls share, and the parameters that go with them.
@@ -830,13 +828,25 @@ static opd_status_t opd_topk_fused_fwd_bwd_impl(const void* z, opd_dtype_t dt, i
                                                 const float* grad_loss, float* loss, float* row_stats, void* dz,
                                                 opd_dtype_t dz_dt, int64_t ld_dz, void* scratch, size_t scratch_bytes,
                                                 void* ws, size_t ws_bytes, hipStream_t stream) {
-  opd_status_t s = check_dz(dz, dz_dt, n_rows, vocab, ld_dz);
+  opd::TopkLossParams p;
+  opd_status_t s = topk_loss_params(z, dt, n_rows, vocab, ld, top_index, top_logit, k, rest_lse, kl, alpha, tau, ws,
+                                    ws_bytes, &p);
   if (s != OPD_OK) return s;
-  s = opd_topk_loss_fwd_impl(z, dt, n_rows, vocab, ld, top_index, top_logit, k, rest_lse, kl, alpha, tau, loss,
-                             row_stats, scratch, scratch_bytes, ws, ws_bytes, stream);
-  if (s != OPD_OK) return s;
-  return opd_topk_loss_bwd_impl(z, dt, n_rows, vocab, ld, top_index, top_logit, k, rest_lse, kl, alpha, tau,
-                                row_stats, grad_loss, dz, dz_dt, ld_dz, ws, ws_bytes, stream);
+  if (n_rows > 0 && (!loss || !row_stats)) return fail(OPD_ERR_NULL, "loss and row_stats must be non-NULL");
+  if ((s = check_dz(dz, dz_dt, n_rows, vocab, ld_dz)) != OPD_OK) return s;
+  if ((s = check_scratch(scratch, scratch_bytes, opd_topk_loss_scratch_size(n_rows, vocab, dt),
+                         "opd_topk_loss_scratch_size()")) != OPD_OK)
+    return s;
+  if (n_rows == 0) return OPD_OK;
+  p.loss = loss;
+  p.row_stats = row_stats;
+  p.seg_lse = static_cast<float*>(scratch);
+  p.grad_loss = grad_loss;
+  p.dz = static_cast<uint8_t*>(dz);
+  p.ld_dz_bytes = ld_dz * (int64_t)dtype_size(dz_dt);
+  hipError_t e = opd::launch_topk_loss_fused(p, dt == OPD_BF16, dz_dt == OPD_BF16, stream);
+  if (e != hipSuccess) return hip_fail(e, "fused top-k loss kernel launch");
+  return OPD_OK;
 }
 
 opd_status_t opd_read_flags(void* ws, size_t ws_bytes, int clear, uint32_t* flags, hipStream_t stream) {

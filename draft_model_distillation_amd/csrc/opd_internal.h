@@ -235,8 +235,10 @@ hipError_t launch_adjust(const AdjustParams& p, int in_bf16, hipStream_t s);  //
 void topk_split(int64_t n_rows, int32_t nvec, int32_t k, int32_t* n_seg, int32_t* seg_vec);
 hipError_t launch_topk(const TopkParams& p, int in_bf16, hipStream_t s);  // opd_topk.hip
 void topk_loss_split(int64_t n_rows, int32_t nvec, int32_t* n_seg, int32_t* seg_vec);
+size_t topk_loss_scratch(int64_t n_rows, int32_t nvec);  // bytes
 hipError_t launch_topk_loss_fwd(const TopkLossParams& p, int in_bf16, hipStream_t s);  // opd_topk_loss.hip
 hipError_t launch_topk_loss_bwd(const TopkLossParams& p, int in_bf16, int out_bf16, hipStream_t s);
+hipError_t launch_topk_loss_fused(const TopkLossParams& p, int in_bf16, int out_bf16, hipStream_t s);
 
 // Records the detail text returned by opd_last_error() on this thread (opd_api.cpp).
 opd_status_t record_error(opd_status_t s, const char* msg);

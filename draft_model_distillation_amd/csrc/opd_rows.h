@@ -27,6 +27,34 @@ __device__ __forceinline__ void store16_nt(uint8_t* p, u32x4 v) {
   __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
 }
 
+// A row as a buffer resource: loads past `bytes` give 0 and stores there are dropped, so that the threads
+// of a workgroup need no test of their own at the row's end. An address is a byte offset of the lane's and
+// one that is the same in every lane; the latter must not pass the end (the hardware takes it off the
+// size), so it is cut off there.
+struct RowBuf {
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t bytes;
+};
+__device__ __forceinline__ RowBuf row_buf(const uint8_t* p, uint32_t bytes) {
+  const uint64_t a = (uint64_t)p;
+  const uint64_t u = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32) |
+                     (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+  const uint32_t n = (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes);
+  return RowBuf{__builtin_amdgcn_make_buffer_rsrc((void*)u, 0, (int)n, 0x00020000), n};
+}
+constexpr int kCached = 0, kStream = 2;  // cache policy: as usual; non-temporal
+template <int POLICY>
+__device__ __forceinline__ u32x4 buf_load16(const RowBuf& b, uint32_t lane_at, uint32_t at) {
+  return __builtin_amdgcn_raw_buffer_load_b128(b.r, (int)lane_at, (int)min(at, b.bytes), POLICY);
+}
+// The whole address of a store is the lane's. A 16-byte store reads its data registers after the next
+// instruction has begun, and the compiler leaves the wait state between it and an instruction that
+// overwrites them only where the store has no scalar offset; with one, the first register has been
+// stored with the next vector's value (seen once in 3e8 elements).
+__device__ __forceinline__ void buf_store16_nt(const RowBuf& b, uint32_t at, u32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, b.r, (int)at, 0, kStream);
+}
+
 // fp32 -> bf16 bits, to nearest, ties to even; NaN stays NaN.
 __device__ __forceinline__ uint32_t bf16_bits(float f) {
   return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f);
@@ -86,25 +114,42 @@ __device__ __forceinline__ void lse_join(float& ref, float& sum, float ref2, flo
   ref = r;
 }
 
-// Joins the pairs of a wave's 64 lanes (a fixed tree; every lane gets the result).
-__device__ __forceinline__ void wave_lse(float& ref, float& sum) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-    const float r2 = __shfl_xor(ref, m), s2 = __shfl_xor(sum, m);
-    lse_join(ref, sum, r2, s2);
-  }
+// Reductions over a wave's 64 lanes, every lane getting the result: four steps inside the rows of 16
+// lanes, then the swaps of rows and halves. The order of additions is fixed.
+template <class F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, F op) {
+  v = op(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));   // lane ^ 1
+  v = op(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));   // lane ^ 2
+  v = op(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true));  // half rows mirrored
+  v = op(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true));  // rows mirrored
+  const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  v = op(p[0], p[1]);
+  const auto q = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)op(q[0], q[1]));
 }
-
 __device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) x += __shfl_xor(x, m);
-  return x;
+  return __uint_as_float(wave_reduce(
+      __float_as_uint(x), [](uint32_t a, uint32_t b) { return __float_as_uint(__uint_as_float(a) + __uint_as_float(b)); }));
+}
+__device__ __forceinline__ float wave_max(float x) {
+  return __uint_as_float(wave_reduce(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+__device__ __forceinline__ int wave_min(int x) {
+  return (int)wave_reduce((uint32_t)x, [](uint32_t a, uint32_t b) { return (uint32_t)min((int)a, (int)b); });
+}
+__device__ __forceinline__ void wave_lse(float& ref, float& sum) {
+  const float r = wave_max(ref);
+  sum = wave_sum(sum * ex2(ref - r));
+  ref = r;
 }
 
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) x = fmaxf(x, __shfl_xor(x, m));
-  return x;
+// A barrier that orders LDS only: global loads and stores stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 }  // namespace opd

@@ -9,9 +9,18 @@
 //   and d_c += (1 - alpha) (p_c - [c = a]); the gradient of a listed token is w d_c, that of any other
 //   token j its share of its class's: w d_rest 2^(z_j log2 e - L), L the log2-sum over the others.
 // So a row costs one exp2 an element for L and one for the gradient, and HBM bounds it. The others'
-// sum leaves the listed tokens out element by element (a bitmap of the segment in LDS names them)
-// instead of subtracting them from the row's sum, which would lose what is left where the drafter has
-// learned the list.
+// sum leaves the listed tokens out element by element (a bitmap in LDS names them) instead of
+// subtracting them from the row's sum, which would lose what is left where the drafter has learned the
+// list. For the same reason the largest class takes no part in the normaliser's sum (its logarithm is
+// that of 1 + the others' sum) and its derivative is minus the sum of the others' (all of them together
+// are 0), which keeps its digits where p and q are both near 1.
+//
+// Kernels:
+//   k_topk_loss_hold  one workgroup per row: the row is loaded once and stays in registers between its
+//                     sum and its gradient (what does not fit is read again, from the caches).
+//   k_topk_loss_sums, k_topk_loss_grad, k_topk_loss_row   a row split into segments with a workgroup
+//                     each, for few rows and for the backward call of its own: sums, then (joining
+//                     them) the gradient or, for the forward call, loss and statistics.
 //
 // This file is compiled with the IEEE mode off, like the row kernels: NaN is outside the contract.
 
@@ -25,135 +34,367 @@
 namespace opd {
 namespace {
 
-constexpr int kSegVec = 4096;   // most vectors of a segment: its bitmap has one byte a vector
-constexpr int kWaves = kThreads / 64;
 constexpr float kLn2 = 0.69314718055994530942f;
-static_assert(kTopkMax <= kThreads, "one thread per listed token");
+constexpr int kSlots = kTopkMax / 64;   // listed tokens per lane of the wave that has the classes
+constexpr int kSegHold = 8;             // vectors per thread of a segment
+constexpr int kSegVec = kThreads * kSegHold;
+constexpr int kLoose = 4;               // vectors in flight per thread of what is not held
 
-struct Shared {
-  int32_t index[kTopkMax];
-  uint32_t listed[kSegVec / 4];  // bit e of byte v: element e of the segment's vector v is listed
-  float red[kWaves][2];
+struct ClassShared {
+  int32_t index[kTopkMax];  // the list's tokens, -1 where an entry does not count
+  float d[kTopkMax];        // their derivatives
+  float L, factor;          // any other token's is factor * 2^(z log2 e - L)
+  float part[16][2];        // the waves' (reference, sum)
 };
 
-__device__ float block_sum(Shared& S, float x) {
-  x = wave_sum(x);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) S.red[threadIdx.x >> 6][0] = x;
-  __syncthreads();
-  float t = S.red[0][0];
-  for (int w = 1; w < kWaves; ++w) t += S.red[w][0];
-  return t;
-}
+// The row's list, entries lane, lane + 64, ... of one wave's lanes.
+struct List {
+  int idx[kSlots];
+  float t[kSlots], z[kSlots];
+};
 
-__device__ float block_max(Shared& S, float x) {
-  x = wave_max(x);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) S.red[threadIdx.x >> 6][0] = x;
-  __syncthreads();
-  float t = S.red[0][0];
-  for (int w = 1; w < kWaves; ++w) t = fmaxf(t, S.red[w][0]);
-  return t;
-}
-
-// Entry threadIdx.x of the row's list: its token, or -1 where there is none that counts.
-__device__ int list_entry(const TopkLossParams& P, Shared& S, int row, bool report) {
-  const int tid = threadIdx.x;
-  int idx = tid < P.k ? P.top_index[(int64_t)row * P.k + tid] : -1;
-  if (idx >= P.vocab) {
-    if (report) atomicOr(P.flags, kFlagBadToken);
-    idx = -1;
-  }
-  if (tid < kTopkMax) S.index[tid] = idx;
-  __syncthreads();
-  bool twice = false;
-  for (int i = 0; i < tid && i < P.k; ++i) twice |= S.index[i] == idx;
-  if (idx >= 0 && twice) {
-    if (report) atomicOr(P.flags, kFlagBadList);
-    idx = -1;
-  }
-  return idx;
-}
-
-// Marks the listed tokens of vectors [v0, v0 + kSegVec) in S.listed.
+// Bit e of vector v of a row's bitmap: element e of the vector is listed (or past the vocabulary).
 template <int EPV>
-__device__ void mark_listed(Shared& S, int idx, int v0) {
-  for (int i = threadIdx.x; i < kSegVec / 4; i += kThreads) S.listed[i] = 0u;
-  __syncthreads();
-  const int v = idx >= 0 ? idx / EPV - v0 : -1;
-  if (v >= 0 && v < kSegVec) atomicOr(&S.listed[v >> 2], 1u << (8 * (v & 3) + idx % EPV));
-  __syncthreads();
+__device__ __forceinline__ uint32_t listed_bits(const uint32_t* listed, int v) {
+  const uint8_t b = reinterpret_cast<const uint8_t*>(listed)[EPV == 8 ? v : v >> 1];
+  return EPV == 8 ? b : (uint32_t)b >> (4 * (v & 1));
 }
 
-// What a row's classes give: thread i has listed token i's derivative, every thread the rest's.
-struct RowResult {
-  float loss, divergence, lse;
-  float d;       // d loss / d z of this thread's listed token
-  float d_rest;  // derivative of the class of all others
+// Words of the bitmap of n vectors.
+__host__ __device__ inline int bitmap_words(int n, int epv) { return (n * epv + 31) / 32; }
+
+// One wave reads the row's list: invalid and repeated entries become -1, the others are marked in the
+// whole row's bitmap (cleared before). Loads of z are left in flight.
+template <bool BF16>
+__device__ void read_list(const TopkLossParams& P, ClassShared& S, uint32_t* listed, int row, bool report, List& li) {
+  const int lane = threadIdx.x & 63;
+  const uint8_t* zr = P.z + (int64_t)row * P.ld_bytes;
+  bool clash = false, bad = false;
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    const int i = s * 64 + lane;
+    li.idx[s] = i < P.k ? P.top_index[(int64_t)row * P.k + i] : -1;
+    li.t[s] = i < P.k ? P.top_logit[(int64_t)row * P.k + i] : kNegInf;
+  }
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    if (li.idx[s] >= P.vocab) {
+      bad = true;
+      li.idx[s] = -1;
+    }
+    if (li.idx[s] >= 0) {
+      const uint32_t bit = 1u << (li.idx[s] & 31);
+      clash |= (atomicOr(&listed[li.idx[s] >> 5], bit) & bit) != 0;
+    }
+  }
+  if (report && bad) atomicOr(P.flags, kFlagBadToken);
+  if (__builtin_amdgcn_ballot_w64(clash)) {  // some token is listed twice: its first entry counts
+    if (report && lane == 0) atomicOr(P.flags, kFlagBadList);
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) S.index[s * 64 + lane] = li.idx[s];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    for (int i = 0; i < P.k; ++i) {
+      const int other = S.index[i];
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s)
+        if (s * 64 + lane > i && li.idx[s] == other) li.idx[s] = -1;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    S.index[s * 64 + lane] = li.idx[s];
+    li.z[s] = li.idx[s] >= 0 ? Vec<BF16>::elem(zr, li.idx[s]) : kNegInf;
+    if (li.idx[s] < 0) li.t[s] = kNegInf;
+  }
+}
+
+// log2(1 + s), s >= 0, to fp32's relative accuracy for small s too: 1 + s rounded to u, corrected by
+// s / (u - 1) (the two differ by as much as the logarithms of 1 + s and u do).
+__device__ __forceinline__ float lg2_1p(float s) {
+  const float u = 1.f + s;
+  return u == 1.f ? s * kLog2e : lg2(u) * (s / (u - 1.f));
+}
+
+// A distribution over the classes from logits x (this lane's listed ones) and (ref, l2), the log2-sum of
+// the others: each class's log2 probability. The largest class's logit is the reference; `top` is its
+// place in the list, -1 if it is that of the others. Returns the log2-sum over all, relative to it.
+struct Dist {
+  float lp[kSlots], lp_rest;
+  float lz;
+  int top;
+};
+__device__ __forceinline__ void distribution(const float (&x)[kSlots], float x_max, int owner, float ref, float l2,
+                                             Dist& D) {
+  const int lane = threadIdx.x & 63;
+  const float above = __builtin_fmaf(x_max, kLog2e, -ref);  // of the largest listed, relative to ref
+  const bool rest_top = l2 > above;
+  D.top = rest_top ? -1 : owner;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    D.lp[i] = rest_top ? __builtin_fmaf(x[i], kLog2e, -ref) - l2 : (x[i] - x_max) * kLog2e;
+    s += i * 64 + lane == D.top ? 0.f : ex2(D.lp[i]);
+  }
+  D.lp_rest = rest_top ? 0.f : l2 - above;
+  s = wave_sum(s) + (rest_top ? 0.f : ex2(D.lp_rest));
+  D.lz = lg2_1p(s);
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) D.lp[i] -= D.lz;
+  D.lp_rest -= D.lz;
+}
+
+// One wave: the row's classes. Puts the derivatives into S and, where `write`, loss and statistics into
+// memory. (ref, sum): the tokens that are not listed.
+__device__ void row_classes(const TopkLossParams& P, ClassShared& S, int row, const List& li, float ref, float l2,
+                            bool write) {
+  const int lane = threadIdx.x & 63;
+  const float inf = __builtin_inff();
+  float t_max = kNegInf, z_max = kNegInf;
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    t_max = fmaxf(t_max, li.t[s]);
+    z_max = fmaxf(z_max, li.z[s]);
+  }
+  t_max = wave_max(t_max);
+  z_max = wave_max(z_max);
+  const int none = 0x7fffffff;
+  int z_own = none, t_own = none, a = none;
+#pragma unroll
+  for (int s = kSlots - 1; s >= 0; --s) {
+    const bool there = li.idx[s] >= 0;
+    if (there && li.z[s] == z_max) z_own = s * 64 + lane;
+    if (there && li.t[s] == t_max) {
+      t_own = s * 64 + lane;
+      a = min(a, li.idx[s]);
+    }
+  }
+  z_own = wave_min(z_own);
+  t_own = wave_min(t_own);
+  a = wave_min(a);  // the teacher's top-1: the lowest token of the largest logit
+  Dist p, q;
+  distribution(li.z, z_max, z_own, ref, l2, p);
+  const float t_rest = P.rest_lse ? P.rest_lse[row] : kNegInf;
+  distribution(li.t, t_max, t_own, t_rest > kNegInf ? t_rest * kLog2e : kNoRef, t_rest > kNegInf ? 0.f : kNegInf, q);
+  const bool active = t_max > kNegInf;  // else nothing is listed and the row takes no part
+  const float alpha = P.alpha, beta = 1.f - alpha;
+
+  // terms, and derivatives but for alpha's common factor S or Q: x_c below (0 ln 0 = 0; a term that is
+  // infinite, the other side's probability being 0, is clipped for any tau)
+  float prob[kSlots], x[kSlots], hard[kSlots];
+  float sum = 0.f, div = 0.f, ce = 0.f, prob_rest, x_rest;
+  const bool reverse = P.kl == OPD_KL_REVERSE;
+  auto one = [&](float lp2, float lq2, float& pr, float& xc) {
+    const float lp = lp2 * kLn2, lq = lq2 * kLn2;
+    pr = ex2(lp2);
+    const float w = reverse ? pr : ex2(lq2);
+    const float l = reverse ? lp - lq : lq - lp;
+    const float term = w > 0.f ? w * l : 0.f;
+    const bool in = term <= P.tau && term < inf && w > 0.f;
+    xc = in ? (reverse ? l + 1.f : w) : 0.f;
+    return fminf(term, P.tau);
+  };
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    const bool there = li.idx[s] >= 0;
+    const float term = one(p.lp[s], q.lp[s], prob[s], x[s]);
+    hard[s] = there && li.idx[s] == a ? 1.f : 0.f;
+    if (there) {
+      div += term;
+      sum += reverse ? prob[s] * x[s] : x[s];
+      if (hard[s] > 0.f) ce = -p.lp[s] * kLn2;
+    }
+  }
+  const float term_rest = one(p.lp_rest, q.lp_rest, prob_rest, x_rest);
+  div = wave_sum(div) + term_rest;
+  sum = wave_sum(sum) + (reverse ? prob_rest * x_rest : x_rest);
+  ce = wave_sum(ce);
+  float d[kSlots], others = 0.f;
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    d[s] = reverse ? prob[s] * (x[s] - sum) : __builtin_fmaf(sum, prob[s], -x[s]);
+    d[s] = li.idx[s] >= 0 ? __builtin_fmaf(alpha, d[s], beta * (prob[s] - hard[s])) : 0.f;
+    others += s * 64 + lane == p.top ? 0.f : d[s];
+  }
+  float d_rest = reverse ? prob_rest * (x_rest - sum) : __builtin_fmaf(sum, prob_rest, -x_rest);
+  d_rest = __builtin_fmaf(alpha, d_rest, beta * prob_rest);
+  others = wave_sum(others) + (p.top < 0 ? 0.f : d_rest);
+  if (p.top < 0) d_rest = -others;
+  const float w = active ? (P.grad_loss ? P.grad_loss[row] : 1.f) : 0.f;
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s)
+    S.d[s * 64 + lane] = active ? w * (s * 64 + lane == p.top ? -others : d[s]) : 0.f;
+  if (lane == 0) {
+    // 2^(z log2 e - L) with L = ref + l2 rounded once, what the rounding lost made up in the factor
+    const bool any = l2 > kNegInf && active;
+    S.L = any ? ref + l2 : 0.f;
+    S.factor = any ? w * d_rest * ex2(l2 - (S.L - ref)) : 0.f;
+    if (write) {
+      P.loss[row] = active ? (alpha > 0.f ? alpha * div : 0.f) + (beta > 0.f ? beta * ce : 0.f) : 0.f;
+      float* st = P.row_stats + 4 * (int64_t)row;
+      st[0] = ref;
+      st[1] = l2;
+      const double base = p.top < 0 ? (double)ref + (double)l2 : (double)z_max * (double)kLog2e;
+      st[2] = (float)((base + (double)p.lz) / (double)kLog2e);
+      st[3] = active ? div : 0.f;
+    }
+  }
+}
+
+// A thread's share of the sum over the tokens that are not listed, kept as sum * 2^ref. The reference
+// may lag the largest exponent by up to 24: 2^24 an element leaves fp32 range to spare.
+struct Rest {
+  float ref = kNoRef, sum = 0.f;
+  template <int EPV>
+  __device__ __forceinline__ void add(float (&x)[EPV], uint32_t out) {
+    if (__builtin_amdgcn_ballot_w64(out != 0u)) {
+#pragma unroll
+      for (int e = 0; e < EPV; ++e) x[e] = (out >> e & 1) ? kNegInf : x[e];
+    }
+    float m = x[0];
+#pragma unroll
+    for (int e = 1; e < EPV; ++e) m = fmaxf(m, x[e]);
+    const float c = m * kLog2e;
+    if (__builtin_amdgcn_ballot_w64(c > ref + 24.f)) {  // (a branch: it is hardly ever taken)
+      const float r = c > ref + 24.f ? c : ref;
+      sum *= ex2(ref - r);
+      ref = r;
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < EPV; ++e) s += ex2(__builtin_fmaf(x[e], kLog2e, -ref));
+    sum += s;
+  }
 };
 
-// rest_ref, rest_l2: reference and log2 of the sum over the tokens not listed.
-template <bool BF16>
-__device__ RowResult row_classes(const TopkLossParams& P, Shared& S, int row, int idx, float rest_ref, float rest_l2) {
-  const int tid = threadIdx.x;
-  const uint8_t* zr = P.z + (int64_t)row * P.ld_bytes;
-  const float t = idx >= 0 ? P.top_logit[(int64_t)row * P.k + tid] : kNegInf;
-  const float z = idx >= 0 ? Vec<BF16>::elem(zr, idx) : kNegInf;
-  const float t_rest = P.rest_lse ? P.rest_lse[row] : kNegInf;
-  RowResult r;
-  const float t_top = block_max(S, t);
-  if (!(t_top > kNegInf)) {  // nothing listed: the row takes no part
-    r.loss = r.divergence = r.d = r.d_rest = 0.f;
-    const float zm = fmaxf(block_max(S, z) * kLog2e, rest_ref);
-    const float sum = block_sum(S, ex2(__builtin_fmaf(z, kLog2e, -zm))) + ex2((rest_ref - zm) + rest_l2);
-    r.lse = (float)(((double)zm + (double)lg2(sum)) / (double)kLog2e);
-    return r;
+// Ends the arithmetic of a held vector here. Without it the compiler holds on to vectors in unpacked form
+// and puts the sums of all of them off together, which costs the registers that the row needs.
+__device__ __forceinline__ void settle(u32x4& v, Rest& r) { asm volatile("" : "+v"(v), "+v"(r.sum), "+v"(r.ref)); }
+
+// Clears the bitmap of n vectors from v0 on and marks the tokens from `end` on. All threads.
+template <int EPV, int T>
+__device__ __forceinline__ void clear_bitmap(uint32_t* listed, int v0, int n, int end) {
+  const int words = bitmap_words(n, EPV), t0 = v0 * EPV;
+  for (int w = threadIdx.x; w < words; w += T) {
+    const int left = end - t0 - 32 * w;
+    listed[w] = left >= 32 ? 0u : left <= 0 ? ~0u : ~0u << left;
   }
-  // the drafter's distribution over the classes
-  const float zm = fmaxf(block_max(S, z) * kLog2e, rest_ref);
-  const float ez = __builtin_fmaf(z, kLog2e, -zm), ez_rest = (rest_ref - zm) + rest_l2;
-  const float lz = lg2(block_sum(S, ex2(ez)) + ex2(ez_rest));
-  r.lse = (float)(((double)zm + (double)lz) / (double)kLog2e);
-  const float lp = (ez - lz) * kLn2, lp_rest = (ez_rest - lz) * kLn2;
-  const float p = ex2(ez - lz), p_rest = ex2(ez_rest - lz);
-  // the teacher's
-  const float tm = fmaxf(t_top, t_rest) * kLog2e;
-  const float et = __builtin_fmaf(t, kLog2e, -tm), et_rest = __builtin_fmaf(t_rest, kLog2e, -tm);
-  const float lt = lg2(block_sum(S, ex2(et)) + ex2(et_rest));
-  const float lq = (et - lt) * kLn2, lq_rest = (et_rest - lt) * kLn2;
-  const float q = ex2(et - lt), q_rest = ex2(et_rest - lt);
-  // its top-1: the lowest token of the largest logit
-  float best = t == t_top ? (float)idx : 3e38f;  // (indices below 2^24 are exact)
-  best = -block_max(S, -best);
-  const float hard = idx >= 0 && (float)idx == best ? 1.f : 0.f;
-  // (0 ln 0 = 0; a listed token of another's probability 0 has an infinite term, clipped for any tau)
-  float term, term_rest, d, d_rest, sum;
-  if (P.kl == OPD_KL_REVERSE) {
-    term = p > 0.f ? p * (lp - lq) : 0.f;
-    term_rest = p_rest > 0.f ? p_rest * (lp_rest - lq_rest) : 0.f;
-    const bool in = term <= P.tau && term < __builtin_inff() && p > 0.f;
-    const bool in_rest = term_rest <= P.tau && term_rest < __builtin_inff() && p_rest > 0.f;
-    const float g = in ? lp - lq + 1.f : 0.f, g_rest = in_rest ? lp_rest - lq_rest + 1.f : 0.f;
-    sum = block_sum(S, p * g) + p_rest * g_rest;
-    d = p * (g - sum);
-    d_rest = p_rest * (g_rest - sum);
+}
+
+// Gradient of one whole vector, tid + v (v the same in every lane), every token as if it were not listed.
+template <bool BF16, bool OUT_BF16>
+__device__ __forceinline__ void grad_vector(const RowBuf& out, int tid, int v, u32x4 raw, float L, float factor) {
+  using V = Vec<BF16>;
+  constexpr int EPV = V::EPV;
+  constexpr uint32_t kBytes = EPV * Vec<OUT_BF16>::SIZE;
+  float x[EPV];
+  V::unpack(raw, x);
+#pragma unroll
+  for (int e = 0; e < EPV; ++e) x[e] = factor * ex2(__builtin_fmaf(x[e], kLog2e, -L));
+  const uint32_t at = (uint32_t)(tid + v) * kBytes;
+  if constexpr (BF16 && !OUT_BF16) {
+    buf_store16_nt(out, at, Vec<false>::pack({x[0], x[1], x[2], x[3]}));
+    buf_store16_nt(out, at + 16, Vec<false>::pack({x[4], x[5], x[6], x[7]}));
+  } else if constexpr (!BF16 && OUT_BF16) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const u32x2 w = {bf16_bits(x[0]) | (bf16_bits(x[1]) << 16), bf16_bits(x[2]) | (bf16_bits(x[3]) << 16)};
+    __builtin_amdgcn_raw_buffer_store_b64(w, out.r, (int)at, 0, kStream);
   } else {
-    term = q > 0.f ? q * (lq - lp) : 0.f;
-    term_rest = q_rest > 0.f ? q_rest * (lq_rest - lp_rest) : 0.f;
-    const float u = term <= P.tau && term < __builtin_inff() ? q : 0.f;
-    const float u_rest = term_rest <= P.tau && term_rest < __builtin_inff() ? q_rest : 0.f;
-    sum = block_sum(S, u) + u_rest;
-    d = __builtin_fmaf(sum, p, -u);
-    d_rest = __builtin_fmaf(sum, p_rest, -u_rest);
+    buf_store16_nt(out, at, V::pack(x));
   }
-  r.divergence = block_sum(S, idx >= 0 ? fminf(term, P.tau) : 0.f) + fminf(term_rest, P.tau);
-  const float ce = -block_sum(S, hard > 0.f ? lp : 0.f);
-  const float beta = 1.f - P.alpha;
-  r.loss = (P.alpha > 0.f ? P.alpha * r.divergence : 0.f) + (beta > 0.f ? beta * ce : 0.f);
-  const float w = P.grad_loss ? P.grad_loss[row] : 1.f;
-  r.d = w * __builtin_fmaf(P.alpha, d, beta * (p - hard));
-  r.d_rest = w * __builtin_fmaf(P.alpha, d_rest, beta * p_rest);
-  return r;
+}
+
+// The elements behind the row's last whole vector, one thread each.
+template <bool BF16, bool OUT_BF16>
+__device__ __forceinline__ void grad_tail(const TopkLossParams& P, const uint8_t* zr, uint8_t* dr, float L, float factor) {
+  const int i = P.vocab / Vec<BF16>::EPV * Vec<BF16>::EPV + (int)threadIdx.x;
+  if (i < P.vocab) Vec<OUT_BF16>::put(dr, i, factor * ex2(__builtin_fmaf(Vec<BF16>::elem(zr, i), kLog2e, -L)));
+}
+
+// Vectors of a row that the loops of k_topk_loss_hold run over: H per thread, then U at a time.
+template <int T, int H, int U>
+__host__ __device__ inline int hold_vectors(int nvec) {
+  const int more = nvec - H * T;
+  return H * T + (more > 0 ? (more + U * T - 1) / (U * T) * (U * T) : 0);
+}
+
+// One workgroup of T threads per row; H vectors per thread stay in registers. GRAD false: the forward
+// call, nothing held.
+template <bool BF16, bool OUT_BF16, bool GRAD, int T, int H>
+__global__ void __launch_bounds__(T) k_topk_loss_hold(TopkLossParams P) {
+  using V = Vec<BF16>;
+  constexpr int EPV = V::EPV;
+  constexpr int U = kLoose;
+  __shared__ ClassShared S;
+  extern __shared__ uint32_t listed[];
+  const int tid = threadIdx.x, row = blockIdx.x;
+  const uint8_t* zr = P.z + (int64_t)row * P.ld_bytes;
+  const int nvec = P.nvec;
+  const RowBuf in = row_buf(zr, (uint32_t)nvec * 16u);
+  u32x4 held[H > 0 ? H : 1];
+#pragma unroll
+  for (int i = 0; i < H; ++i) held[i] = buf_load16<kStream>(in, (uint32_t)tid * 16u, (uint32_t)(i * T) * 16u);
+  clear_bitmap<EPV, T>(listed, 0, hold_vectors<T, H, U>(nvec), P.vocab);
+  lds_barrier();
+  List li;
+  if (tid < 64) read_list<BF16>(P, S, listed, row, true, li);
+  lds_barrier();
+  Rest rest;
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    float x[EPV];
+    V::unpack(held[i], x);
+    rest.add<EPV>(x, listed_bits<EPV>(listed, i * T + tid));
+    settle(held[i], rest);
+  }
+  for (int v0 = H * T; v0 < nvec; v0 += U * T) {
+    u32x4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u] = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)(v0 + u * T) * 16u);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float x[EPV];
+      V::unpack(raw[u], x);
+      rest.add<EPV>(x, listed_bits<EPV>(listed, v0 + u * T + tid));
+      settle(raw[u], rest);
+    }
+  }
+  wave_lse(rest.ref, rest.sum);
+  if ((tid & 63) == 0) {
+    S.part[tid >> 6][0] = rest.ref;
+    S.part[tid >> 6][1] = rest.sum;
+  }
+  lds_barrier();
+  if (tid < 64) {
+    float ref = tid < T / 64 ? S.part[tid][0] : kNoRef;
+    float sum = tid < T / 64 ? S.part[tid][1] : 0.f;
+    wave_lse(ref, sum);
+    row_classes(P, S, row, li, ref, sum > 0.f ? lg2(sum) : kNegInf, true);
+  }
+  if constexpr (GRAD) {
+    lds_barrier();
+    const float L = S.L, factor = S.factor;
+    uint8_t* dr = P.dz + (int64_t)row * P.ld_dz_bytes;
+    const RowBuf out = row_buf(dr, (uint32_t)(P.vocab / EPV) * (uint32_t)(EPV * Vec<OUT_BF16>::SIZE));
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      grad_vector<BF16, OUT_BF16>(out, tid, i * T, held[i], L, factor);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    for (int v0 = H * T; v0 < nvec; v0 += U * T) {
+      u32x4 raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) raw[u] = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)(v0 + u * T) * 16u);
+#pragma unroll
+      for (int u = 0; u < U; ++u) grad_vector<BF16, OUT_BF16>(out, tid, v0 + u * T, raw[u], L, factor);
+    }
+    grad_tail<BF16, OUT_BF16>(P, zr, dr, L, factor);
+    __syncthreads();  // the listed tokens' places are written over, after all the others' stores
+    for (int i = tid; i < P.k; i += T) {
+      const int idx = S.index[i];
+      if (idx >= 0) Vec<OUT_BF16>::put(dr, idx, S.d[i]);
+    }
+  }
 }
 
 // One workgroup per (row, segment): reference and sum of the segment's tokens that are not listed.
@@ -161,100 +402,174 @@ template <bool BF16>
 __global__ void __launch_bounds__(kThreads) k_topk_loss_sums(TopkLossParams P) {
   using V = Vec<BF16>;
   constexpr int EPV = V::EPV;
-  __shared__ Shared S;
+  __shared__ float part[kThreads / 64][2];
+  __shared__ uint32_t listed[kSegVec * EPV / 32];
   const int tid = threadIdx.x;
   const int row = blockIdx.x / P.n_seg, seg = blockIdx.x - row * P.n_seg;
   const uint8_t* zr = P.z + (int64_t)row * P.ld_bytes;
   const int v0 = seg * P.seg_vec, v1 = min(v0 + P.seg_vec, P.nvec);
-  const int idx = list_entry(P, S, row, false);
-  mark_listed<EPV>(S, idx, v0);
-  float ref = kNoRef, sum = 0.f;
-  for (int v = v0 + tid; v < v1; v += kThreads) {
+  const RowBuf in = row_buf(zr, (uint32_t)v1 * 16u);
+  u32x4 held[kSegHold];
+#pragma unroll
+  for (int i = 0; i < kSegHold; ++i) held[i] = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)(v0 + i * kThreads) * 16u);
+  clear_bitmap<EPV, kThreads>(listed, v0, kSegVec, min(v1 * EPV, P.vocab));
+  lds_barrier();
+  for (int i = tid; i < P.k; i += kThreads) {
+    const int t = P.top_index[(int64_t)row * P.k + i];
+    const int at = t - v0 * EPV;
+    if (t >= 0 && t < P.vocab && at >= 0 && at < (v1 - v0) * EPV) atomicOr(&listed[at >> 5], 1u << (at & 31));
+  }
+  lds_barrier();
+  Rest rest;
+#pragma unroll
+  for (int i = 0; i < kSegHold; ++i) {
     float x[EPV];
-    V::unpack(load16(zr + (int64_t)v * 16), x);
-    const uint32_t out = reinterpret_cast<const uint8_t*>(S.listed)[v - v0];
-    float m = kNegInf;
-#pragma unroll
-    for (int e = 0; e < EPV; ++e) {
-      if ((out >> e & 1) || v * EPV + e >= P.vocab) x[e] = kNegInf;
-      m = fmaxf(m, x[e]);
-    }
-    const float c = m * kLog2e;
-    if (c > ref + 24.f) {  // (the sum's exponents stay below 24 + the number of terms' logarithm)
-      sum *= ex2(ref - c);
-      ref = c;
-    }
-#pragma unroll
-    for (int e = 0; e < EPV; ++e) sum += ex2(__builtin_fmaf(x[e], kLog2e, -ref));
+    V::unpack(held[i], x);
+    rest.add<EPV>(x, listed_bits<EPV>(listed, i * kThreads + tid));
+    settle(held[i], rest);
   }
-  wave_lse(ref, sum);
+  wave_lse(rest.ref, rest.sum);
   if ((tid & 63) == 0) {
-    S.red[tid >> 6][0] = ref;
-    S.red[tid >> 6][1] = sum;
+    part[tid >> 6][0] = rest.ref;
+    part[tid >> 6][1] = rest.sum;
   }
-  __syncthreads();
+  lds_barrier();
   if (tid == 0) {
-    for (int w = 1; w < kWaves; ++w) lse_join(ref, sum, S.red[w][0], S.red[w][1]);
+    float ref = part[0][0], sum = part[0][1];
+    for (int w = 1; w < kThreads / 64; ++w) lse_join(ref, sum, part[w][0], part[w][1]);
     P.seg_lse[2 * (int64_t)blockIdx.x] = ref;
     P.seg_lse[2 * (int64_t)blockIdx.x + 1] = sum;
   }
 }
 
-// One workgroup per row: joins the segments' sums; loss and statistics.
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads) k_topk_loss_row(TopkLossParams P) {
-  __shared__ Shared S;
-  const int tid = threadIdx.x, row = blockIdx.x;
-  const int idx = list_entry(P, S, row, true);
-  float ref = kNoRef, sum = 0.f;
-  for (int i = 0; i < P.n_seg; ++i) {  // every thread the same additions
+// One wave joins a row's segments (lane i takes segments i, i + 64, ...).
+__device__ void join_segments(const TopkLossParams& P, int row, float& ref, float& l2) {
+  float sum = 0.f;
+  ref = kNoRef;
+  for (int i = threadIdx.x & 63; i < P.n_seg; i += 64) {
     const float* p = P.seg_lse + 2 * ((int64_t)row * P.n_seg + i);
     lse_join(ref, sum, p[0], p[1]);
   }
-  const float l2 = sum > 0.f ? lg2(sum) : kNegInf;
-  const RowResult r = row_classes<BF16>(P, S, row, idx, ref, l2);
-  if (tid == 0) {
-    P.loss[row] = r.loss;
-    float* st = P.row_stats + 4 * (int64_t)row;
-    st[0] = ref;
-    st[1] = l2;
-    st[2] = r.lse;
-    st[3] = r.divergence;
-  }
+  wave_lse(ref, sum);
+  l2 = sum > 0.f ? lg2(sum) : kNegInf;
 }
 
-// One workgroup per (row, segment): the gradient.
-template <bool BF16, bool OUT_BF16>
+// One wave per row: joins the segments' sums; loss and statistics.
+template <bool BF16>
+__global__ void __launch_bounds__(64) k_topk_loss_row(TopkLossParams P) {
+  __shared__ ClassShared S;
+  extern __shared__ uint32_t listed[];
+  const int row = blockIdx.x;
+  clear_bitmap<Vec<BF16>::EPV, 64>(listed, 0, P.nvec, P.vocab);
+  lds_barrier();
+  List li;
+  read_list<BF16>(P, S, listed, row, true, li);
+  float ref, l2;
+  join_segments(P, row, ref, l2);
+  row_classes(P, S, row, li, ref, l2, true);
+}
+
+// One workgroup per (row, segment): the gradient. JOIN: from the segments' sums, the first segment's
+// workgroup writing loss and statistics (the fused call); else from the statistics (the backward call).
+template <bool BF16, bool OUT_BF16, bool JOIN>
 __global__ void __launch_bounds__(kThreads) k_topk_loss_grad(TopkLossParams P) {
   using V = Vec<BF16>;
-  using O = Vec<OUT_BF16>;
   constexpr int EPV = V::EPV;
-  __shared__ Shared S;
+  __shared__ ClassShared S;
+  extern __shared__ uint32_t listed[];
   const int tid = threadIdx.x;
   const int row = blockIdx.x / P.n_seg, seg = blockIdx.x - row * P.n_seg;
   const uint8_t* zr = P.z + (int64_t)row * P.ld_bytes;
   uint8_t* dr = P.dz + (int64_t)row * P.ld_dz_bytes;
   const int v0 = seg * P.seg_vec, v1 = min(v0 + P.seg_vec, P.nvec);
-  const int idx = list_entry(P, S, row, false);
-  const float ref = P.row_stats[4 * (int64_t)row], l2 = P.row_stats[4 * (int64_t)row + 1];
-  const RowResult r = row_classes<BF16>(P, S, row, idx, ref, l2);
-  // 2^(z log2 e - L) with L = ref + l2 rounded once, and what the rounding lost made up in the factor
-  const bool others = l2 > kNegInf;
-  const float L = others ? ref + l2 : 0.f;
-  const float factor = others ? r.d_rest * ex2(l2 - (L - ref)) : 0.f;
-  for (int v = v0 + tid; v < v1; v += kThreads) {
-    float x[EPV];
-    V::unpack(load16(zr + (int64_t)v * 16), x);
+  const RowBuf in = row_buf(zr, (uint32_t)v1 * 16u);
+  u32x4 held[kSegHold];
 #pragma unroll
-    for (int e = 0; e < EPV; ++e) x[e] = others ? factor * ex2(__builtin_fmaf(x[e], kLog2e, -L)) : 0.f;
-    const int valid = P.vocab - v * EPV;
-#pragma unroll
-    for (int e = 0; e < EPV; ++e)
-      if (e < valid) O::put(dr, v * EPV + e, x[e]);
+  for (int i = 0; i < kSegHold; ++i) held[i] = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)(v0 + i * kThreads) * 16u);
+  clear_bitmap<EPV, kThreads>(listed, 0, P.nvec, P.vocab);
+  lds_barrier();
+  if (tid < 64) {
+    List li;
+    read_list<BF16>(P, S, listed, row, JOIN && seg == 0, li);
+    float ref, l2;
+    if constexpr (JOIN) {
+      join_segments(P, row, ref, l2);
+    } else {
+      ref = P.row_stats[4 * (int64_t)row];
+      l2 = P.row_stats[4 * (int64_t)row + 1];
+    }
+    row_classes(P, S, row, li, ref, l2, JOIN && seg == 0);
   }
-  __syncthreads();  // the listed tokens' places are written over, in this order
-  const int v = idx >= 0 ? idx / EPV : -1;
-  if (v >= v0 && v < v1) O::put(dr, idx, r.d);
+  lds_barrier();
+  const float L = S.L, factor = S.factor;
+  // (the segment's end cuts the output off too: behind it the next workgroup writes)
+  const RowBuf out = row_buf(dr, (uint32_t)min(v1, P.vocab / EPV) * (uint32_t)(EPV * Vec<OUT_BF16>::SIZE));
+#pragma unroll
+  for (int i = 0; i < kSegHold; ++i) {
+    grad_vector<BF16, OUT_BF16>(out, tid, v0 + i * kThreads, held[i], L, factor);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (seg == P.n_seg - 1) grad_tail<BF16, OUT_BF16>(P, zr, dr, L, factor);
+  __syncthreads();  // the listed tokens' places are written over, after all the others' stores
+  for (int i = tid; i < P.k; i += kThreads) {
+    const int idx = S.index[i];
+    if (idx >= v0 * EPV && idx < v1 * EPV) Vec<OUT_BF16>::put(dr, idx, S.d[i]);
+  }
+}
+
+constexpr int kHoldRows = 128;  // rows from which a workgroup per row is faster than split rows
+
+// Launches a kernel with a row's bitmap in LDS (above 64 KiB with the kernel's own for the widest rows,
+// which has to be allowed; the setting is per device, so it is made on every such launch).
+template <class K>
+hipError_t launch_with_bitmap(K kernel, int64_t grid, int threads, int vectors, int epv, const TopkLossParams& p,
+                              hipStream_t s) {
+  const size_t lds = 4 * (size_t)bitmap_words(vectors, epv);
+  if (lds + sizeof(ClassShared) > 64 * 1024) {
+    const hipError_t e =
+        hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3((unsigned)threads), lds, s, p);
+  return hipGetLastError();
+}
+
+template <bool BF16, bool OUT_BF16, bool GRAD, int T, int H>
+hipError_t launch_hold(const TopkLossParams& p, hipStream_t s) {
+  return launch_with_bitmap(k_topk_loss_hold<BF16, OUT_BF16, GRAD, T, H>, p.n_rows, T,
+                            hold_vectors<T, H, kLoose>(p.nvec), Vec<BF16>::EPV, p, s);
+}
+
+template <bool BF16, bool OUT_BF16, bool JOIN>
+hipError_t launch_grad(const TopkLossParams& p, hipStream_t s) {
+  return launch_with_bitmap(k_topk_loss_grad<BF16, OUT_BF16, JOIN>, (int64_t)p.n_rows * p.n_seg, kThreads, p.nvec,
+                            Vec<BF16>::EPV, p, s);
+}
+
+template <bool BF16>
+hipError_t launch_sums(const TopkLossParams& p, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)p.n_rows * p.n_seg));
+  hipLaunchKernelGGL(k_topk_loss_sums<BF16>, grid, dim3(kThreads), 0, s, p);
+  return hipGetLastError();
+}
+
+template <bool BF16, bool OUT_BF16>
+hipError_t launch_fused(const TopkLossParams& p, hipStream_t s) {
+  if (p.n_rows >= kHoldRows) {
+    if (p.nvec <= 256 * 16) return launch_hold<BF16, OUT_BF16, true, 256, 16>(p, s);
+    if (p.nvec <= 512 * 19) return launch_hold<BF16, OUT_BF16, true, 512, 19>(p, s);
+    return launch_hold<BF16, OUT_BF16, true, 1024, 19>(p, s);
+  }
+  const hipError_t e = launch_sums<BF16>(p, s);
+  return e != hipSuccess ? e : launch_grad<BF16, OUT_BF16, true>(p, s);
+}
+
+template <bool BF16>
+hipError_t launch_fwd(const TopkLossParams& p, hipStream_t s) {
+  if (p.n_rows >= kHoldRows) return launch_hold<BF16, false, false, 512, 0>(p, s);
+  const hipError_t e = launch_sums<BF16>(p, s);
+  if (e != hipSuccess) return e;
+  return launch_with_bitmap(k_topk_loss_row<BF16>, p.n_rows, 64, p.nvec, Vec<BF16>::EPV, p, s);
 }
 
 }  // namespace
@@ -262,38 +577,31 @@ __global__ void __launch_bounds__(kThreads) k_topk_loss_grad(TopkLossParams P) {
 void topk_loss_split(int64_t n_rows, int32_t nvec, int32_t* n_seg, int32_t* seg_vec) {
   // Segments of at most kSegVec vectors; more of them where the rows alone do not fill the device.
   int64_t seg = n_rows > 0 ? (1024 + n_rows - 1) / n_rows : 1;
-  seg = std::min<int64_t>(seg, (nvec + 2 * kThreads - 1) / (2 * kThreads));
+  seg = std::min<int64_t>(seg, (nvec + kThreads - 1) / kThreads);
   seg = std::max<int64_t>(seg, (nvec + kSegVec - 1) / kSegVec);
-  *seg_vec = (int32_t)((nvec + seg - 1) / seg);
+  *seg_vec = (int32_t)(((nvec + seg - 1) / seg + 7) / 8 * 8);  // (whole bitmap words and 128-byte lines)
   *n_seg = (nvec + *seg_vec - 1) / *seg_vec;
 }
 
+size_t topk_loss_scratch(int64_t n_rows, int32_t nvec) {
+  if (n_rows >= kHoldRows) return 0;
+  int32_t seg = 1, seg_vec = 0;
+  topk_loss_split(n_rows, nvec, &seg, &seg_vec);
+  return (size_t)n_rows * seg * 8;
+}
+
 hipError_t launch_topk_loss_fwd(const TopkLossParams& p, int in_bf16, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)p.n_rows * p.n_seg));
-  if (in_bf16)
-    hipLaunchKernelGGL(k_topk_loss_sums<true>, grid, dim3(kThreads), 0, s, p);
-  else
-    hipLaunchKernelGGL(k_topk_loss_sums<false>, grid, dim3(kThreads), 0, s, p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (in_bf16)
-    hipLaunchKernelGGL(k_topk_loss_row<true>, dim3((unsigned)p.n_rows), dim3(kThreads), 0, s, p);
-  else
-    hipLaunchKernelGGL(k_topk_loss_row<false>, dim3((unsigned)p.n_rows), dim3(kThreads), 0, s, p);
-  return hipGetLastError();
+  return in_bf16 ? launch_fwd<true>(p, s) : launch_fwd<false>(p, s);
 }
 
 hipError_t launch_topk_loss_bwd(const TopkLossParams& p, int in_bf16, int out_bf16, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)p.n_rows * p.n_seg));
-  if (in_bf16 && out_bf16)
-    hipLaunchKernelGGL((k_topk_loss_grad<true, true>), grid, dim3(kThreads), 0, s, p);
-  else if (in_bf16)
-    hipLaunchKernelGGL((k_topk_loss_grad<true, false>), grid, dim3(kThreads), 0, s, p);
-  else if (out_bf16)
-    hipLaunchKernelGGL((k_topk_loss_grad<false, true>), grid, dim3(kThreads), 0, s, p);
-  else
-    hipLaunchKernelGGL((k_topk_loss_grad<false, false>), grid, dim3(kThreads), 0, s, p);
-  return hipGetLastError();
+  if (in_bf16) return out_bf16 ? launch_grad<true, true, false>(p, s) : launch_grad<true, false, false>(p, s);
+  return out_bf16 ? launch_grad<false, true, false>(p, s) : launch_grad<false, false, false>(p, s);
+}
+
+hipError_t launch_topk_loss_fused(const TopkLossParams& p, int in_bf16, int out_bf16, hipStream_t s) {
+  if (in_bf16) return out_bf16 ? launch_fused<true, true>(p, s) : launch_fused<true, false>(p, s);
+  return out_bf16 ? launch_fused<false, true>(p, s) : launch_fused<false, false>(p, s);
 }
 
 }  // namespace opd

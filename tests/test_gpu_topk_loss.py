@@ -163,6 +163,40 @@ def test_row_counts_split_differently(lib, rows, V, dtype):
            rows=sorted({0, rows // 3, rows // 2, rows - 1}))
 
 
+@pytest.mark.parametrize("rows", [3, 130])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_widest_rows(lib, dtype, rows):
+    y, z, _ = _rows(14, 2, 524288)
+    pick = np.arange(rows) % 2
+    idx, logit, rest = _lists(y, 256)
+    _check(lib, z[pick], idx[pick], logit[pick], rest[pick], dtype=dtype, dz=dtype, rows=[0, rows - 1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_rows_same_bits_every_time(lib, dtype):
+    import torch
+
+    g = torch.Generator(device="cuda").manual_seed(3)
+    z = torch.randn(600, synth.VOCAB, device="cuda", generator=g).mul_(4).to(
+        torch.float32 if dtype == "f32" else torch.bfloat16)
+    kept = lib.topk_rows(z, 64)
+    first = None
+    for _ in range(4):
+        out = lib.topk_fused_fwd_bwd(z, kept["index"], kept["values"] * 0.5, kept["rest_lse"], 0.7, 0.02, dz_dtype=torch.float32)
+        torch.cuda.synchronize()
+        if first is None:
+            first = out
+        assert torch.equal(out["dz"], first["dz"]) and torch.equal(out["loss"], first["loss"])
+    # the gradient of a softmax adds up to 0 along each row
+    total = first["dz"].double().sum(1).abs().max()
+    assert float(total) <= 1e-5
+    split = lib.topk_loss_fwd(z, kept["index"], kept["values"] * 0.5, kept["rest_lse"], 0.7, 0.02)
+    dz = lib.topk_loss_bwd(z, kept["index"], kept["values"] * 0.5, kept["rest_lse"], 0.7, 0.02, split[1],
+                           dz_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert float((dz - first["dz"]).abs().max()) <= 1e-5
+
+
 @pytest.mark.parametrize("kl", ["reverse", "forward"])
 def test_gradient_against_differences(lib, kl):
     # A central difference is off by h^2 / 6 times the third derivative. A class's term p l has the third
