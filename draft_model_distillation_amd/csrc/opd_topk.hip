@@ -1,17 +1,20 @@
 // The k largest logits of every row and the log-sum-exp of all the others, in one pass over the row.
 //
-// A workgroup takes a segment of a row (the whole row where there are rows enough to fill the
-// device). The k-th largest of the threads' maxima over their first vectors is a lower bound t of the
-// k-th largest logit; from there on an element above the bound is a candidate and goes, as a 64-bit
-// key (value's order in the upper half, falling index in the lower, so that no two are the same),
-// into a buffer in LDS, and any other adds 2^(x log2 e - ref) to its thread's sum. Candidates are few
-// (for random order about k per group-sized part of the segment). When the buffer could run over, it
-// is sorted, the k largest stay, the bound rises to the k-th, and the others join the sums; the end
-// does the same. The sum of the others is never formed by subtracting the listed ones, which would
-// lose what is left where the list holds nearly all of the row.
+// A workgroup takes a segment of a row (the whole row where there are rows enough to fill the device).
+// Its first vectors are loaded into registers at once; the k-th largest of the maxima of groups of
+// threads over them is a lower bound of the k-th largest logit. From there on an element at or above the
+// bound is a candidate and goes, as a 64-bit key (value's order in the upper half, falling index in the
+// lower, so that no two are the same), into a buffer in LDS, and any other adds 2^(x log2 e - ref) to its
+// thread's sum; what is not in registers is streamed past the same bound. Where the whole row is held
+// (a bf16 row of 151,936 logits is), candidates are little more than k. They are ranked by counting, the
+// k largest are the answer, and the others join the sums in the order of their rank. The sum of the
+// others is never formed by subtracting the listed ones, which would lose what is left where the list
+// holds nearly all of the row.
 //
-// Every set and every order of additions depends on the data alone, not on the order in which
-// candidates reach the buffer, so results are the same bits every time.
+// When the buffer would run over (rows of equal values; rising rows), it is cut to the k largest and the
+// bound raised to the k-th, after every few vectors if need be. Every set and every order of additions
+// depends on the data alone, not on the order in which candidates reach the buffer, so results are the
+// same bits every time.
 //
 // This file is compiled with the IEEE mode off, like the row kernels: NaN is outside the contract.
 
@@ -25,7 +28,10 @@
 namespace opd {
 namespace {
 
-constexpr int kGroupVec = 4;  // vectors per thread between two checks of the buffer
+constexpr int kLoose = 4;        // vectors in flight per thread of what is not held
+constexpr int kBatch = 256;      // threads that append between two checks where the buffer runs over
+constexpr int kRankMost = 512;   // candidates up to which ranking by counting beats sorting
+constexpr uint32_t kKeyNegInf = 0x007fffffu;
 
 // Unsigned keys in the order of the values (-0 as +0, so that equal values go by index).
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -39,86 +45,131 @@ __device__ __forceinline__ uint64_t make_key(float x, int index) {
   return ((uint64_t)order_key(x) << 32) | (uint32_t)~index;
 }
 
-// A thread's share of the log-sum-exp of the elements that are not listed: sum * 2^ref.
+// A thread's share of the log-sum-exp of the elements that are not listed: sum * 2^ref. The reference
+// may lag the largest exponent by up to 24: 2^24 an element leaves fp32 range to spare.
 struct Rest {
   float ref = kNoRef, sum = 0.f;
-  // ref may lag the largest exponent by up to 24: 2^24 an element leaves fp32 range to spare
   __device__ __forceinline__ void raise(float m) {
     const float c = m * kLog2e;
-    if (c > ref + 24.f) {
-      sum *= ex2(ref - c);
-      ref = c;
+    if (__builtin_amdgcn_ballot_w64(c > ref + 24.f)) {  // (a branch: it is hardly ever taken)
+      const float r = c > ref + 24.f ? c : ref;
+      sum *= ex2(ref - r);
+      ref = r;
     }
   }
-  __device__ __forceinline__ void add(float x) { sum += ex2(__builtin_fmaf(x, kLog2e, -ref)); }
+  __device__ __forceinline__ float term(float x) const { return ex2(__builtin_fmaf(x, kLog2e, -ref)); }
 };
+
+// Ends the arithmetic of a vector here: the compiler would otherwise keep vectors in unpacked form and put
+// their sums off together, which costs the registers that the row needs.
+__device__ __forceinline__ void settle(u32x4& v, Rest& r) { asm volatile("" : "+v"(v), "+v"(r.sum), "+v"(r.ref)); }
 
 struct Shared {
   uint64_t keys[kTopkCap];
-  float part[kThreads];
-  float pair[kThreads / 64][2];
+  uint64_t sorted[kRankMost];
+  uint32_t maxima[512];
+  float pair[16][2];
   float bound;
   int count;
 };
 
-// Sorts the n buffered keys (largest first), keeps the k largest, and adds the others to the threads'
-// sums in the order of their rank. Returns the number kept. All threads call it.
-__device__ int settle(Shared& S, int n, int k, Rest& rest) {
+// The first bound: the k-th largest of m maxima' keys in S.maxima (one wave; m a multiple of 64), as far as
+// its upper `bits` bits say, rounded down; -inf where there are not k.
+template <int M>
+__device__ void find_bound(Shared& S, int k, int bits) {
+  const int lane = threadIdx.x & 63;
+  uint32_t key[M / 64];
+#pragma unroll
+  for (int i = 0; i < M / 64; ++i) key[i] = S.maxima[i * 64 + lane];
+  uint32_t p = 0;
+  for (int b = 31; b >= 32 - bits; --b) {
+    const uint32_t q = p | (1u << b);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < M / 64; ++i) n += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[i] >= q));
+    if (n >= k) p = q;
+  }
+  if (lane == 0) S.bound = key_value(max(p, kKeyNegInf));
+}
+
+// Orders the n keys in S.keys (largest first), keeps the k largest there and adds the others to the
+// threads' sums in the order of their rank. Returns the number kept; S.bound is the k-th's value. All T
+// threads call it.
+template <int T>
+__device__ int cut(Shared& S, int n, int k, Rest& rest) {
   const int tid = threadIdx.x;
-  int m = 2;
-  while (m < n) m <<= 1;
-  for (int i = n + tid; i < m; i += kThreads) S.keys[i] = 0;
-  __syncthreads();
-  for (int size = 2; size <= m; size <<= 1)
-    for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      for (int i = tid; i < m / 2; i += kThreads) {
-        const int a = 2 * i - (i & (stride - 1)), b = a + stride;
-        const uint64_t x = S.keys[a], y = S.keys[b];
-        const bool falling = (a & size) == 0;
-        if ((x < y) == falling) {
-          S.keys[a] = y;
-          S.keys[b] = x;
-        }
-      }
-      __syncthreads();
+  const uint64_t* from = S.keys;
+  if (n <= kRankMost) {
+    for (int i = tid; i < n; i += T) {
+      const uint64_t mine = S.keys[i];
+      int rank = 0;
+      for (int j = 0; j < n; ++j) rank += S.keys[j] > mine ? 1 : 0;
+      S.sorted[rank] = mine;
     }
-  for (int i = k + tid; i < n; i += kThreads) {
-    if (S.keys[i] == 0) continue;  // (a segment's list that was not full)
-    const float x = key_value((uint32_t)(S.keys[i] >> 32));
-    rest.raise(x);
-    rest.add(x);
+    lds_barrier();
+    from = S.sorted;
+  } else {
+    int m = 1024;
+    while (m < n) m <<= 1;
+    for (int i = n + tid; i < m; i += T) S.keys[i] = 0;
+    lds_barrier();
+    for (int size = 2; size <= m; size <<= 1)
+      for (int stride = size >> 1; stride > 0; stride >>= 1) {
+        for (int i = tid; i < m / 2; i += T) {
+          const int a = 2 * i - (i & (stride - 1)), b = a + stride;
+          const uint64_t x = S.keys[a], y = S.keys[b];
+          if ((x < y) == ((a & size) == 0)) {
+            S.keys[a] = y;
+            S.keys[b] = x;
+          }
+        }
+        lds_barrier();
+      }
+  }
+  for (int i = k + tid; i < n; i += T) {
+    const float x = key_value((uint32_t)(from[i] >> 32));
+    const float c = x * kLog2e;
+    if (c > rest.ref + 24.f) {
+      rest.sum *= ex2(rest.ref - c);
+      rest.ref = c;
+    }
+    rest.sum += rest.term(x);
   }
   const int kept = min(n, k);
+  if (from != S.keys)
+    for (int i = tid; i < kept; i += T) S.keys[i] = from[i];
   if (tid == 0) {
     S.count = kept;
-    S.bound = n >= k ? key_value((uint32_t)(S.keys[k - 1] >> 32)) : kNegInf;
+    S.bound = n >= k ? key_value((uint32_t)(from[k - 1] >> 32)) : kNegInf;
   }
-  __syncthreads();
+  lds_barrier();
   return kept;
 }
 
-// Joins the threads' sums; thread 0 has the result.
+// Joins the threads' sums; the first wave has the result.
+template <int T>
 __device__ void join_rest(Shared& S, Rest& rest) {
+  const int tid = threadIdx.x;
   wave_lse(rest.ref, rest.sum);
-  if ((threadIdx.x & 63) == 0) {
-    S.pair[threadIdx.x >> 6][0] = rest.ref;
-    S.pair[threadIdx.x >> 6][1] = rest.sum;
+  if ((tid & 63) == 0) {
+    S.pair[tid >> 6][0] = rest.ref;
+    S.pair[tid >> 6][1] = rest.sum;
   }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    rest.ref = S.pair[0][0];
-    rest.sum = S.pair[0][1];
-    for (int w = 1; w < kThreads / 64; ++w) lse_join(rest.ref, rest.sum, S.pair[w][0], S.pair[w][1]);
+  lds_barrier();
+  if (tid < 64) {
+    rest.ref = tid < T / 64 ? S.pair[tid][0] : kNoRef;
+    rest.sum = tid < T / 64 ? S.pair[tid][1] : 0.f;
+    wave_lse(rest.ref, rest.sum);
   }
 }
 
 // Writes a row's answer: the first `kept` keys (an entry that is not there: index -1) and the sum.
+template <int T>
 __device__ void write_row(const TopkParams& P, const Shared& S, int row, int kept, const Rest& rest) {
-  for (int i = threadIdx.x; i < P.k; i += kThreads) {
+  for (int i = threadIdx.x; i < P.k; i += T) {
     const uint64_t key = i < kept ? S.keys[i] : 0;
-    const bool there = key != 0;
-    P.values[(int64_t)row * P.k + i] = there ? key_value((uint32_t)(key >> 32)) : kNegInf;
-    P.index[(int64_t)row * P.k + i] = there ? (int32_t)~(uint32_t)key : -1;
+    P.values[(int64_t)row * P.k + i] = key ? key_value((uint32_t)(key >> 32)) : kNegInf;
+    P.index[(int64_t)row * P.k + i] = key ? (int32_t)~(uint32_t)key : -1;
   }
   if (threadIdx.x == 0)  // the exponents are of fp32's log2(e), so that one is divided out
     P.rest_lse[row] = rest.sum > 0.f
@@ -126,143 +177,197 @@ __device__ void write_row(const TopkParams& P, const Shared& S, int row, int kep
                           : kNegInf;
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads) k_topk(TopkParams P) {
+// What a workgroup knows while it goes over its segment. Until the buffer has once been cut to k, an
+// element equal to the bound may belong to the list; from then on it cannot: k keys at or above the
+// bound are held, and its index is higher than theirs.
+struct Bound {
+  float at;
+  bool strict;
+  __device__ __forceinline__ bool above(float x) const { return strict ? x > at : x >= at; }
+};
+
+// One vector: candidates into the buffer, the others into the sum.
+template <int EPV>
+__device__ __forceinline__ void take(Shared& S, const Bound& B, Rest& rest, const float (&x)[EPV], int first, int end) {
+  float m = x[0];
+#pragma unroll
+  for (int e = 1; e < EPV; ++e) m = fmaxf(m, x[e]);
+  if (__builtin_amdgcn_ballot_w64(m >= B.at)) {
+    float o = kNegInf;  // the largest of those that are no candidates
+    float y[EPV];
+#pragma unroll
+    for (int e = 0; e < EPV; ++e) {
+      const bool cand = B.above(x[e]);
+      if (cand && first + e < end) {
+        const int at = atomicAdd(&S.count, 1);
+        if (at < kTopkCap) S.keys[at] = make_key(x[e], first + e);
+      }
+      y[e] = cand ? kNegInf : x[e];
+      o = fmaxf(o, y[e]);
+    }
+    rest.raise(o);
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < EPV; ++e) s += rest.term(y[e]);
+    rest.sum += s;
+  } else {
+    rest.raise(m);
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < EPV; ++e) s += rest.term(x[e]);
+    rest.sum += s;
+  }
+}
+
+// The candidates of one vector per thread again, in batches of threads, cutting the buffer before it could
+// run over (`was`: the bound that take() went by; the others are in the sum already). All threads.
+template <int EPV, int T>
+__device__ void take_again(Shared& S, Bound& B, const Bound& was, Rest& rest, const float (&x)[EPV], int first, int end,
+                           int& n, int k) {
+  for (int b = 0; b < T / kBatch; ++b) {
+    if (n + kBatch * EPV > kTopkCap) {
+      n = cut<T>(S, n, k, rest);
+      if (n == k) B = Bound{S.bound, true};
+    }
+    if ((int)threadIdx.x / kBatch == b) {
+#pragma unroll
+      for (int e = 0; e < EPV; ++e)
+        if (was.above(x[e]) && first + e < end) {
+          if (B.above(x[e])) {
+            S.keys[atomicAdd(&S.count, 1)] = make_key(x[e], first + e);
+          } else {
+            const float c = x[e] * kLog2e;
+            if (c > rest.ref + 24.f) {
+              rest.sum *= ex2(rest.ref - c);
+              rest.ref = c;
+            }
+            rest.sum += rest.term(x[e]);
+          }
+        }
+    }
+    lds_barrier();
+    n = S.count;
+    lds_barrier();
+  }
+}
+
+// One workgroup of T threads per (row, segment); H vectors per thread are held. M: maxima that the first
+// bound is found from.
+template <bool BF16, int T, int H, int M>
+__global__ void __launch_bounds__(T) k_topk(TopkParams P) {
   using V = Vec<BF16>;
   constexpr int EPV = V::EPV;
+  constexpr int U = kLoose;
   __shared__ Shared S;
   const int tid = threadIdx.x;
   const int row = blockIdx.x / P.n_seg, seg = blockIdx.x - row * P.n_seg;
-  const uint8_t* yr = P.y + (int64_t)row * P.ld_bytes;
-  const int v0 = seg * P.seg_vec, v1 = min(v0 + P.seg_vec, P.nvec);
-  const int k = P.k;
-  Rest rest;
+  const int v0 = seg * P.seg_vec, n_vec = min(P.seg_vec, P.nvec - v0), k = P.k;
+  const int base = v0 * EPV, end = min((v0 + n_vec) * EPV, P.vocab);  // tokens [base, end)
+  const RowBuf in = row_buf(P.y + (int64_t)row * P.ld_bytes + (int64_t)v0 * 16, (uint32_t)n_vec * 16u);
   if (tid == 0) S.count = 0;
 
-  u32x4 raw[kGroupVec];
-  auto load = [&](int g0) {
+  // Vector v + tid; its elements past the segment's end become -inf.
+  auto unpack = [&](u32x4& raw, int v, float (&x)[EPV]) {
+    V::unpack(raw, x);
+    if (base + (v + T) * EPV > end) {
 #pragma unroll
-    for (int u = 0; u < kGroupVec; ++u) {
-      const int v = g0 + u * kThreads + tid;
-      raw[u] = v < v1 ? load16_nt(yr + (int64_t)v * 16) : u32x4{0, 0, 0, 0};
+      for (int e = 0; e < EPV; ++e) x[e] = base + (v + tid) * EPV + e < end ? x[e] : kNegInf;
     }
   };
-  // Elements of vector v, NaN-free; those past the vocabulary are not there (`valid` of them are).
-  auto valid_of = [&](int v) { return v < v1 ? min(EPV, P.vocab - v * EPV) : 0; };
 
-  load(v0);
-  {  // the first bound: the k-th largest of the threads' maxima
-    float m = kNegInf;
+  u32x4 held[H];
 #pragma unroll
-    for (int u = 0; u < kGroupVec; ++u) {
-      const int valid = valid_of(v0 + u * kThreads + tid);
+  for (int i = 0; i < H; ++i) held[i] = buf_load16<kStream>(in, (uint32_t)tid * 16u, (uint32_t)(i * T) * 16u);
+  float m = kNegInf;
+#pragma unroll
+  for (int i = 0; i < H; ++i)
+    if (i * T < n_vec) {
       float x[EPV];
-      V::unpack(raw[u], x);
+      unpack(held[i], i * T, x);
 #pragma unroll
-      for (int e = 0; e < EPV; ++e)
-        if (e < valid) m = fmaxf(m, x[e]);
+      for (int e = 0; e < EPV; ++e) m = fmaxf(m, x[e]);
+      asm volatile("" : "+v"(held[i]), "+v"(m));
     }
-    S.part[tid] = m;
-    __syncthreads();
-    int above = 0;
-    for (int i = 0; i < kThreads; ++i) {
-      const float o = S.part[i];
-      above += (o > m || (o == m && i < tid)) ? 1 : 0;
-    }
-    if (above == k - 1) S.bound = m;
-    __syncthreads();
+  {
+    constexpr int G = T / M;  // threads per maximum: neighbours
+    float g = m;
+    if (G >= 2) g = fmaxf(g, __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(g), 0xB1, 0xF, 0xF, true)));
+    if (G >= 4) g = fmaxf(g, __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(g), 0x4E, 0xF, 0xF, true)));
+    static_assert(G == 1 || G == 2 || G == 4, "maxima of one, two or four lanes");
+    // (-inf is also what a group without elements has: no maximum, so that fewer than k of them are seen)
+    if (tid % G == 0) S.maxima[tid / G] = g > kNegInf ? order_key(g) : 0u;
   }
-  float bound = S.bound;
-  // Until the buffer has once been cut to k, an element equal to the bound may belong to the list;
-  // from then on it cannot: k keys at or above the bound are held, and its index is higher than theirs.
-  bool strict = false;
+  lds_barrier();
+  if (tid < 64) find_bound<M>(S, k, BF16 ? 16 : 24);
+  lds_barrier();
+  Bound B{S.bound, false};
   int n = 0;
-  auto above = [&](float x) { return strict ? x > bound : x >= bound; };
-  auto append = [&](float x, int index) {
-    const int at = atomicAdd(&S.count, 1);
-    if (at < kTopkCap) S.keys[at] = make_key(x, index);
-  };
-
-  for (int g0 = v0; g0 < v1; g0 += kThreads * kGroupVec) {
-    if (g0 != v0) load(g0);
+  Rest rest;
+  rest.ref = m > kNegInf && m < B.at ? m * kLog2e : kNoRef;  // no candidate among the thread's: m is its largest
 #pragma unroll
-    for (int u = 0; u < kGroupVec; ++u) {
-      const int v = g0 + u * kThreads + tid;
-      const int valid = valid_of(v);
+  for (int i = 0; i < H; ++i)
+    if (i * T < n_vec) {
       float x[EPV];
-      V::unpack(raw[u], x);
-      float m = kNegInf;
-#pragma unroll
-      for (int e = 0; e < EPV; ++e)
-        if (e < valid && !above(x[e])) m = fmaxf(m, x[e]);
-      rest.raise(m);
-#pragma unroll
-      for (int e = 0; e < EPV; ++e)
-        if (e < valid) {
-          if (above(x[e]))
-            append(x[e], v * EPV + e);
-          else
-            rest.add(x[e]);
-        }
+      unpack(held[i], i * T, x);
+      take<EPV>(S, B, rest, x, base + (i * T + tid) * EPV, end);
+      settle(held[i], rest);
     }
-    __syncthreads();
+  lds_barrier();
+  n = S.count;
+  lds_barrier();
+  if (n > kTopkCap) {
+    if (tid == 0) S.count = 0;
+    lds_barrier();
+    n = 0;
+    const Bound was = B;
+#pragma unroll 1
+    for (int i = 0; i * T < n_vec && i < H; ++i) {
+      // (read again: held[i] with i not a constant would put the row into memory)
+      u32x4 raw = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)(i * T) * 16u);
+      float x[EPV];
+      unpack(raw, i * T, x);
+      take_again<EPV, T>(S, B, was, rest, x, base + (i * T + tid) * EPV, end, n, k);
+    }
+  }
+  for (int g0 = H * T; g0 < n_vec; g0 += U * T) {
+    u32x4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u] = buf_load16<kStream>(in, (uint32_t)tid * 16u, (uint32_t)(g0 + u * T) * 16u);
+    if (n > kTopkCap / 4) {
+      n = cut<T>(S, n, k, rest);
+      if (n == k) B = Bound{S.bound, true};
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float x[EPV];
+      unpack(raw[u], g0 + u * T, x);
+      take<EPV>(S, B, rest, x, base + (g0 + u * T + tid) * EPV, end);
+      settle(raw[u], rest);
+    }
+    lds_barrier();
     const int total = S.count;
-    __syncthreads();
+    lds_barrier();
     if (total <= kTopkCap) {
       n = total;
-      if (n > kTopkCap / 2) {
-        n = settle(S, n, k, rest);
-        if (n == k) {
-          bound = S.bound;
-          strict = true;
-        }
-      }
       continue;
     }
-    // More candidates than places: back to the n keys of before the group, then one vector per thread
-    // at a time, cutting before the buffer could run over.
-    const float old_bound = bound;
-    const bool old_strict = strict;
-    __syncthreads();
     if (tid == 0) S.count = n;
-    __syncthreads();
+    lds_barrier();
+    const Bound was = B;
 #pragma unroll
-    for (int u = 0; u < kGroupVec; ++u) {
-      if (n + kThreads * EPV > kTopkCap) {
-        n = settle(S, n, k, rest);
-        if (n == k) {
-          bound = S.bound;
-          strict = true;
-        }
-      }
-      const int v = g0 + u * kThreads + tid;
-      const int valid = valid_of(v);
+    for (int u = 0; u < U; ++u) {
       float x[EPV];
-      V::unpack(raw[u], x);
-#pragma unroll
-      for (int e = 0; e < EPV; ++e) {
-        const bool was = old_strict ? x[e] > old_bound : x[e] >= old_bound;
-        if (e < valid && was) {  // (the others are in the sum already)
-          if (above(x[e])) {
-            append(x[e], v * EPV + e);
-          } else {
-            rest.raise(x[e]);
-            rest.add(x[e]);
-          }
-        }
-      }
-      __syncthreads();
-      n = S.count;
-      __syncthreads();
+      unpack(raw[u], g0 + u * T, x);
+      take_again<EPV, T>(S, B, was, rest, x, base + (g0 + u * T + tid) * EPV, end, n, k);
     }
   }
-  const int kept = settle(S, n, k, rest);
-  join_rest(S, rest);
+  const int kept = cut<T>(S, n, k, rest);
+  join_rest<T>(S, rest);
   if (P.n_seg == 1) {
-    write_row(P, S, row, kept, rest);
+    write_row<T>(P, S, row, kept, rest);
   } else {
     uint64_t* keys = P.seg_keys + (int64_t)blockIdx.x * k;
-    for (int i = tid; i < k; i += kThreads) keys[i] = i < kept ? S.keys[i] : 0;
+    for (int i = tid; i < k; i += T) keys[i] = i < kept ? S.keys[i] : 0;
     if (tid == 0) {
       P.seg_lse[2 * (int64_t)blockIdx.x] = rest.ref;
       P.seg_lse[2 * (int64_t)blockIdx.x + 1] = rest.sum;
@@ -270,44 +375,86 @@ __global__ void __launch_bounds__(kThreads) k_topk(TopkParams P) {
   }
 }
 
-// One workgroup per row: the segments' keys together are few enough to be sorted at once.
+// One workgroup per row joins the segments' lists and sums: again a bound from the threads' maxima, the keys
+// at or above it ranked, the others added to the sums by the threads that loaded them.
 __global__ void __launch_bounds__(kThreads) k_topk_merge(TopkParams P) {
+  constexpr int T = kThreads, R = kTopkCap / T;
   __shared__ Shared S;
-  const int tid = threadIdx.x, row = blockIdx.x;
-  const int total = P.n_seg * P.k;
+  const int tid = threadIdx.x, row = blockIdx.x, k = P.k;
+  const int total = P.n_seg * k;
   const uint64_t* keys = P.seg_keys + (int64_t)row * total;
-  for (int i = tid; i < total; i += kThreads) S.keys[i] = keys[i];
+  uint64_t mine[R];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    mine[i] = i * T + tid < total ? keys[i * T + tid] : 0;
+    m = max(m, (uint32_t)(mine[i] >> 32));
+  }
   Rest rest;
-  for (int i = tid; i < P.n_seg; i += kThreads) {
+  for (int i = tid; i < P.n_seg; i += T) {
     const float* p = P.seg_lse + 2 * ((int64_t)row * P.n_seg + i);
     lse_join(rest.ref, rest.sum, p[0], p[1]);
   }
-  __syncthreads();
-  const int kept = settle(S, total, P.k, rest);
-  join_rest(S, rest);
-  write_row(P, S, row, kept, rest);
+  if (tid == 0) S.count = 0;
+  S.maxima[tid] = m;
+  lds_barrier();
+  if (tid < 64) find_bound<T>(S, k, 32);
+  lds_barrier();
+  const float bound = S.bound;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (mine[i] == 0) continue;  // (a list that was not full)
+    const float x = key_value((uint32_t)(mine[i] >> 32));
+    if (x >= bound) {
+      S.keys[atomicAdd(&S.count, 1)] = mine[i];
+    } else {
+      const float c = x * kLog2e;
+      if (c > rest.ref + 24.f) {
+        rest.sum *= ex2(rest.ref - c);
+        rest.ref = c;
+      }
+      rest.sum += rest.term(x);
+    }
+  }
+  lds_barrier();
+  const int kept = cut<T>(S, S.count, k, rest);
+  join_rest<T>(S, rest);
+  write_row<T>(P, S, row, kept, rest);
+}
+
+constexpr int kWholeRows = 192;  // rows from which a workgroup per row is faster than split rows
+
+template <bool BF16, int T, int H, int M>
+hipError_t launch(const TopkParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((k_topk<BF16, T, H, M>), dim3((unsigned)((int64_t)p.n_rows * p.n_seg)), dim3(T), 0, s, p);
+  return hipGetLastError();
+}
+
+template <bool BF16>
+hipError_t launch_rows(const TopkParams& p, hipStream_t s) {
+  if (p.seg_vec <= 256 * 8) return launch<BF16, 256, 8, 256>(p, s);
+  if (p.seg_vec <= 512 * 10) return launch<BF16, 512, 10, 512>(p, s);
+  return p.k <= 96 ? launch<BF16, 1024, 19, 256>(p, s) : launch<BF16, 1024, 19, 512>(p, s);
 }
 
 }  // namespace
 
 void topk_split(int64_t n_rows, int32_t nvec, int32_t k, int32_t* n_seg, int32_t* seg_vec) {
-  // One workgroup per row once the rows alone give every CU two; with fewer, enough segments for that,
-  // of at least two vectors per thread, and at most as many as one workgroup can merge.
-  int64_t seg = n_rows > 0 ? (512 + n_rows - 1) / n_rows : 1;
-  seg = std::min<int64_t>(seg, (nvec + 2 * kThreads - 1) / (2 * kThreads));
-  seg = std::min<int64_t>(seg, kTopkCap / k);
-  seg = std::max<int64_t>(seg, 1);
-  *seg_vec = (int32_t)((nvec + seg - 1) / seg);
+  // Few rows: segments for two workgroups of 256 threads per CU, of at least four vectors per thread, and at
+  // most as many as one workgroup can merge.
+  int64_t seg = 1;
+  if (n_rows > 0 && n_rows < kWholeRows) {
+    seg = (1024 + n_rows - 1) / n_rows;
+    seg = std::min<int64_t>(seg, (nvec + 4 * kThreads - 1) / (4 * kThreads));
+    seg = std::min<int64_t>(seg, kTopkCap / k);
+    seg = std::max<int64_t>(seg, 1);
+  }
+  *seg_vec = (int32_t)(((nvec + seg - 1) / seg + 7) / 8 * 8);
   *n_seg = (nvec + *seg_vec - 1) / *seg_vec;
 }
 
 hipError_t launch_topk(const TopkParams& p, int in_bf16, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)p.n_rows * p.n_seg));
-  if (in_bf16)
-    hipLaunchKernelGGL(k_topk<true>, grid, dim3(kThreads), 0, s, p);
-  else
-    hipLaunchKernelGGL(k_topk<false>, grid, dim3(kThreads), 0, s, p);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = in_bf16 ? launch_rows<true>(p, s) : launch_rows<false>(p, s);
   if (e != hipSuccess || p.n_seg == 1) return e;
   hipLaunchKernelGGL(k_topk_merge, dim3((unsigned)p.n_rows), dim3(kThreads), 0, s, p);
   return hipGetLastError();

@@ -341,12 +341,13 @@ __global__ void __launch_bounds__(T) k_topk_loss_hold(TopkLossParams P) {
   lds_barrier();
   Rest rest;
 #pragma unroll
-  for (int i = 0; i < H; ++i) {
-    float x[EPV];
-    V::unpack(held[i], x);
-    rest.add<EPV>(x, listed_bits<EPV>(listed, i * T + tid));
-    settle(held[i], rest);
-  }
+  for (int i = 0; i < H; ++i)
+    if (i * T < nvec) {
+      float x[EPV];
+      V::unpack(held[i], x);
+      rest.add<EPV>(x, listed_bits<EPV>(listed, i * T + tid));
+      settle(held[i], rest);
+    }
   for (int v0 = H * T; v0 < nvec; v0 += U * T) {
     u32x4 raw[U];
 #pragma unroll
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(T) k_topk_loss_hold(TopkLossParams P) {
     const RowBuf out = row_buf(dr, (uint32_t)(P.vocab / EPV) * (uint32_t)(EPV * Vec<OUT_BF16>::SIZE));
 #pragma unroll
     for (int i = 0; i < H; ++i) {
-      grad_vector<BF16, OUT_BF16>(out, tid, i * T, held[i], L, factor);
+      if (i * T < nvec) grad_vector<BF16, OUT_BF16>(out, tid, i * T, held[i], L, factor);
       __builtin_amdgcn_sched_barrier(0);
     }
     for (int v0 = H * T; v0 < nvec; v0 += U * T) {
