@@ -8,8 +8,9 @@
 // their own. A workgroup takes a tile of one block's vocabulary and all of the block's rows (or
 // every gridDim.z-th group of kRowGroup rows): it scans the request's history once, counting the
 // tile's tokens in LDS, turns the counts into one fp32 number to subtract and two bits per token
-// (known; counted in the output), and streams its rows past that state. The proposals of a block's
-// earlier rows are added on the way, by the thread that holds the token.
+// (known; counted in the output), and streams its rows past that state, several vectors in flight per
+// thread. The proposals of a block's earlier rows are added on the way, by the thread that holds the
+// token. (A history of H tokens is read by every tile, from the L2: 4 H bytes a tile against 32 KB a row.)
 
 #include <stdint.h>
 
@@ -19,8 +20,9 @@
 namespace opd {
 namespace {
 
-constexpr int kTileVec = 1024;  // 16-byte vectors of a row that a workgroup takes
+constexpr int kTileVec = 1024;  // most 16-byte vectors of a row that a workgroup takes
 constexpr int kRowGroup = 16;   // rows of a block that share one scan of the history
+constexpr int kAhead = 4;       // vectors in flight per thread
 
 __device__ __forceinline__ int clamp_len(const int32_t* p, int b, int most, bool* bad) {
   const int n = p ? p[b] : most;
@@ -28,48 +30,50 @@ __device__ __forceinline__ int clamp_len(const int32_t* p, int b, int most, bool
   return min(max(n, 0), most);
 }
 
-template <bool BF16>
+// Whether a block's rows have a mask that allows nothing, or a number that is none.
+__device__ void check_masks(const AdjustParams& P, int start, int nb) {
+  const int tid = threadIdx.x;
+  for (int j0 = blockIdx.z * kRowGroup; j0 < nb; j0 += gridDim.z * kRowGroup)
+    for (int j = j0; j < min(j0 + kRowGroup, nb); ++j) {
+      const int mr = P.mask_row ? P.mask_row[start + j] : start + j;
+      if (mr < 0) continue;
+      if (mr >= P.n_masks) {
+        if (tid == 0) atomicOr(P.flags, kFlagBadList);
+        continue;
+      }
+      const uint32_t* m = reinterpret_cast<const uint32_t*>(P.mask + (int64_t)mr * P.ld_mask_bytes);
+      const int words = (P.vocab + 31) / 32;
+      bool any = false;
+      for (int w0 = 0; w0 < words && !any; w0 += kThreads) {
+        const int w = w0 + tid;
+        uint32_t bits = w < words ? m[w] : 0u;
+        if (w == words - 1 && (P.vocab & 31)) bits &= (1u << (P.vocab & 31)) - 1u;
+        any = __syncthreads_or(bits != 0u);
+      }
+      if (!any && tid == 0) atomicOr(P.flags, kFlagEmptyMask);
+    }
+}
+
+// STATE: with penalties or biases (else masks alone, and no LDS).
+template <bool BF16, bool STATE>
 __global__ void __launch_bounds__(kThreads) k_adjust(AdjustParams P) {
   using V = Vec<BF16>;
   constexpr int EPV = V::EPV;
-  constexpr int kTok = kTileVec * EPV;
+  constexpr int kTok = STATE ? kTileVec * EPV : 64;
   __shared__ float sub[kTok];  // first a bias entry's number, then the token's count, then what to subtract
-  __shared__ uint32_t known[kTok / 32], counted[kTok / 32];
-  const int b = blockIdx.y, tid = threadIdx.x;
+  __shared__ uint64_t known[kTok / 64], counted[kTok / 64];
+  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
   const int start = P.offsets[b], end = P.offsets[b + 1];
-  const bool first = blockIdx.x == 0 && blockIdx.z == 0;
   if (start < 0 || end < start || end > P.n_rows) {
-    if (first && tid == 0) atomicOr(P.flags, kFlagBadOffsets);
+    if (blockIdx.x == 0 && blockIdx.z == 0 && tid == 0) atomicOr(P.flags, kFlagBadOffsets);
     return;
   }
   const int nb = end - start;
-  const int v0 = blockIdx.x * kTileVec;
-  const int v1 = min(v0 + kTileVec, P.nvec);
+  if ((int)blockIdx.x == P.tiles) return check_masks(P, start, nb);  // the workgroups behind the tiles
+  const int v0 = blockIdx.x * P.tile_vec;
+  const int nv = min(P.tile_vec, P.nvec - v0);  // vectors of the tile
   const int t0 = v0 * EPV;
-  const unsigned nt = (unsigned)(min(v1 * EPV, P.vocab) - t0);  // tokens of the tile
-
-  if ((int)blockIdx.x == (int)gridDim.x - 1 && P.mask) {  // the last tile's workgroup is for empty masks
-    for (int j0 = blockIdx.z * kRowGroup; j0 < nb; j0 += gridDim.z * kRowGroup)
-      for (int j = j0; j < min(j0 + kRowGroup, nb); ++j) {
-        const int mr = P.mask_row ? P.mask_row[start + j] : start + j;
-        if (mr < 0) continue;
-        if (mr >= P.n_masks) {
-          if (tid == 0) atomicOr(P.flags, kFlagBadList);
-          continue;
-        }
-        const uint32_t* m = reinterpret_cast<const uint32_t*>(P.mask + (int64_t)mr * P.ld_mask_bytes);
-        const int words = (P.vocab + 31) / 32;
-        bool any = false;
-        for (int w0 = 0; w0 < words && !any; w0 += kThreads) {
-          const int w = w0 + tid;
-          uint32_t bits = w < words ? m[w] : 0u;
-          if (w == words - 1 && (P.vocab & 31)) bits &= (1u << (P.vocab & 31)) - 1u;
-          any = __syncthreads_or(bits != 0u);
-        }
-        if (!any && tid == 0) atomicOr(P.flags, kFlagEmptyMask);
-      }
-    return;
-  }
+  const unsigned nt = (unsigned)(min((v0 + nv) * EPV, P.vocab) - t0);  // tokens of the tile
 
   const float rho = P.repetition ? P.repetition[b] : 1.f;
   const float inv_rho = 1.f / rho;
@@ -87,105 +91,172 @@ __global__ void __launch_bounds__(kThreads) k_adjust(AdjustParams P) {
 
   for (int j0 = blockIdx.z * kRowGroup; j0 < nb; j0 += gridDim.z * kRowGroup) {
     const int rows = min(kRowGroup, nb - j0);
-    __syncthreads();  // the previous group's rows are done with the state
-    for (int i = tid; i < kTok; i += kThreads) count[i] = 0u;
-    for (int i = tid; i < kTok / 32; i += kThreads) known[i] = counted[i] = 0u;
-    __syncthreads();
-    // Which bias entries count: the last of a token's, found as the largest number in its slot.
-    uint64_t mine = 0;  // entries tid, tid + kThreads, ... of this thread that count
-    if (n_bias) {
-      for (int i = tid; i < n_bias; i += kThreads) {
-        const unsigned t = (unsigned)(btok[i] - t0);
-        if ((unsigned)btok[i] >= (unsigned)P.vocab) bad_token = true;
-        else if (t < nt) atomicMax(&count[t], (uint32_t)i + 1u);
+    if constexpr (STATE) {
+      __syncthreads();  // the previous group's rows are done with the state
+      for (int i = tid; i < nv * EPV; i += kThreads) count[i] = 0u;
+      for (int i = tid; i < kTok / 64; i += kThreads) known[i] = 0u;
+      __syncthreads();
+      // Which bias entries count: the last of a token's, found as the largest number in its slot.
+      uint64_t mine = 0;  // entries tid, tid + kThreads, ... of this thread that count
+      if (n_bias) {
+        for (int i = tid; i < n_bias; i += kThreads) {
+          const unsigned t = (unsigned)(btok[i] - t0);
+          if ((unsigned)btok[i] >= (unsigned)P.vocab) bad_token = true;
+          else if (t < nt) atomicMax(&count[t], (uint32_t)i + 1u);
+        }
+        __syncthreads();
+        int q = 0;
+        for (int i = tid; i < n_bias; i += kThreads, ++q) {
+          const unsigned t = (unsigned)(btok[i] - t0);
+          if ((unsigned)btok[i] < (unsigned)P.vocab && t < nt && count[t] == (uint32_t)i + 1u) mine |= 1ull << q;
+        }
+        __syncthreads();
+        q = 0;
+        for (int i = tid; i < n_bias; i += kThreads, ++q)
+          if (mine >> q & 1) count[btok[i] - t0] = 0u;
+        __syncthreads();
+      }
+      // Counts: the history, then the proposals of the block's rows before this group.
+      auto see = [&](int tok, bool prompt) {
+        bad_token |= (unsigned)tok >= (unsigned)P.vocab;
+        const unsigned t = (unsigned)(tok - t0);
+        if (t < nt && (unsigned)tok < (unsigned)P.vocab) {
+          if (prompt)
+            atomicOr(reinterpret_cast<uint32_t*>(known) + (t >> 5), 1u << (t & 31));
+          else
+            atomicAdd(&count[t], 1u);
+        }
+      };
+      constexpr int Q = 16;  // tokens in flight per thread
+      int i = 0;
+      for (; i + Q * kThreads <= n_hist; i += Q * kThreads) {
+        struct alignas(4) Four { int32_t t[4]; };  // (16 bytes at once, of any row pitch)
+        Four f[Q / 4];
+#pragma unroll
+        for (int q = 0; q < Q / 4; ++q) f[q] = *reinterpret_cast<const Four*>(hist + i + 4 * (q * kThreads + tid));
+#pragma unroll
+        for (int q = 0; q < Q / 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) see(f[q].t[e], i + 4 * (q * kThreads + tid) + e < n_prompt);
+      }
+#pragma unroll 4
+      for (int h = i + tid; h < n_hist; h += kThreads) see(hist[h], h < n_prompt);
+      if (P.draft)
+        for (int h = tid; h < j0; h += kThreads) see(P.draft[start + h], false);
+      __syncthreads();
+      for (int t = tid; t < (nv * EPV + 63) / 64 * 64; t += kThreads) {
+        const uint32_t c = t < nv * EPV ? count[t] : 0u;
+        if (t < nv * EPV) sub[t] = c ? __builtin_fmaf(freq, (float)c, pres) : 0.f;
+        const uint64_t bits = __builtin_amdgcn_ballot_w64(c != 0u);
+        if (lane == 0) {
+          counted[t >> 6] = bits;
+          known[t >> 6] |= bits;
+        }
       }
       __syncthreads();
-      int q = 0;
-      for (int i = tid; i < n_bias; i += kThreads, ++q) {
-        const unsigned t = (unsigned)(btok[i] - t0);
-        if ((unsigned)btok[i] < (unsigned)P.vocab && t < nt && count[t] == (uint32_t)i + 1u) mine |= 1ull << q;
+      if (mine) {
+        int q = 0;
+        for (int k = tid; k < n_bias; k += kThreads, ++q)
+          if (mine >> q & 1) sub[btok[k] - t0] -= bval[k];
       }
       __syncthreads();
-      q = 0;
-      for (int i = tid; i < n_bias; i += kThreads, ++q)
-        if (mine >> q & 1) count[btok[i] - t0] = 0u;
-      __syncthreads();
     }
-    // Counts: the history, then the proposals of the block's rows before this group.
-    const int n_draft = P.draft ? j0 : 0;
-    for (int i = tid; i < n_hist + n_draft; i += kThreads) {
-      const int tok = i < n_hist ? hist[i] : P.draft[start + i - n_hist];
-      if ((unsigned)tok >= (unsigned)P.vocab) {
-        bad_token = true;
-        continue;
-      }
-      const unsigned t = (unsigned)(tok - t0);
-      if (t < nt) {
-        atomicOr(&known[t >> 5], 1u << (t & 31));
-        if (i >= n_prompt) atomicAdd(&count[t], 1u);
-      }
-    }
-    __syncthreads();
-    for (int w = tid; w < kTok / 32; w += kThreads) {
-      uint32_t bits = 0;
-      for (int i = 0; i < 32; ++i) {
-        const uint32_t c = count[32 * w + i];
-        sub[32 * w + i] = c ? __builtin_fmaf(freq, (float)c, pres) : 0.f;
-        bits |= (c ? 1u : 0u) << i;
-      }
-      counted[w] = bits;
-    }
-    __syncthreads();
-    if (mine) {
-      int q = 0;
-      for (int i = tid; i < n_bias; i += kThreads, ++q)
-        if (mine >> q & 1) sub[btok[i] - t0] -= bval[i];
-    }
-    __syncthreads();
 
-    for (int v = v0 + tid; v < v1; v += kThreads) {
-      const int e0 = (v - v0) * EPV;
-      float s[EPV];
-#pragma unroll
-      for (int e = 0; e < EPV; ++e) s[e] = sub[e0 + e];
-      uint32_t kn = known[e0 >> 5] >> (e0 & 31), co = counted[e0 >> 5] >> (e0 & 31);
-      const int valid = P.vocab - v * EPV;
-      for (int j = 0; j < rows; ++j) {
-        const int row = start + j0 + j;
-        if (j && P.draft) {  // the previous row's proposal is part of the output from here on
-          const int tok = P.draft[row - 1] - t0 - e0;
-#pragma unroll
-          for (int e = 0; e < EPV; ++e)
-            if (tok == e && e < valid) {
-              s[e] += freq + ((co >> e & 1) ? 0.f : pres);
-              co |= 1u << e;
-              kn |= 1u << e;
-            }
-        }
-        float x[EPV];
-        V::unpack(load16(P.x + (int64_t)row * P.ld_bytes + (int64_t)v * 16), x);
-        uint32_t allowed = 0xffu;
-        if (P.mask) {
-          const int mr = P.mask_row ? P.mask_row[row] : row;
-          if (mr >= 0 && mr < P.n_masks) {
-            const uint8_t* m = P.mask + (int64_t)mr * P.ld_mask_bytes;
-            allowed = BF16 ? m[v] : (uint32_t)m[v >> 1] >> (4 * (v & 1));
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-          const float mul = (kn >> e & 1) ? (x[e] > 0.f ? inv_rho : rho) : 1.f;
-          x[e] = (allowed >> e & 1) ? __builtin_fmaf(x[e], mul, -s[e]) : P.masked_value;
-        }
-        uint8_t* o = P.out + (int64_t)row * P.ld_out_bytes;
-        if (valid >= EPV) {
-          store16_nt(o + (int64_t)v * 16, V::pack(x));
-        } else {
-#pragma unroll
-          for (int e = 0; e < EPV; ++e)
-            if (e < valid) V::put(o, v * EPV + e, x[e]);
-        }
+    // Lane j: the proposal before the group's row j, and the row's mask (one that is none: -1).
+    const int mine_row = start + j0 + lane;
+    const int lane_tok = STATE && P.draft && lane < rows && j0 + lane > 0 ? P.draft[mine_row - 1] : -1;
+    int lane_mask = -1;
+    if (P.mask && lane < rows) lane_mask = P.mask_row ? P.mask_row[mine_row] : mine_row;
+    if (lane_mask >= P.n_masks) lane_mask = -1;
+
+    // The tile's vectors, kThreads at a time, and for each the group's rows: items (u, j) in that order,
+    // kAhead of them loaded ahead of the one that is worked on.
+    const int n_u = (nv + kThreads - 1) / kThreads, items = n_u * rows;
+    u32x4 raw[kAhead];
+    uint32_t bits[kAhead];
+    int load_u = 0, load_j = 0, u = 0, j = 0;
+    auto load = [&](u32x4& to, uint32_t& allowed) {
+      const int64_t row = start + j0 + load_j;
+      const RowBuf in = row_buf(P.x + row * P.ld_bytes + (int64_t)v0 * 16, (uint32_t)nv * 16u);
+      to = buf_load16<kStream>(in, (uint32_t)tid * 16u, (uint32_t)(load_u * kThreads) * 16u);
+      if (P.mask) {
+        const int mr = __builtin_amdgcn_readlane(lane_mask, load_j);
+        // a bf16 vector has a byte of the mask, an fp32 vector half of one; without a mask nothing is read
+        const int64_t first = BF16 ? v0 : v0 >> 1;
+        const RowBuf m = row_buf(P.mask + max(mr, 0) * P.ld_mask_bytes + first,
+                                 mr < 0 ? 0u : (uint32_t)(BF16 ? nv : (nv + 1) >> 1));
+        const uint32_t at = (uint32_t)(BF16 ? load_u * kThreads : load_u * kThreads / 2);
+        const uint32_t byte = __builtin_amdgcn_raw_buffer_load_b8(m.r, BF16 ? tid : tid >> 1, (int)min(at, m.bytes), 0);
+        allowed = BF16 ? byte : byte >> (4 * (tid & 1));
       }
+      if (++load_j == rows) {
+        load_j = 0;
+        ++load_u;
+      }
+    };
+    float s[EPV], up[EPV], down[EPV];  // what to subtract; factors of a positive and of another logit
+    uint32_t kn = 0, co = 0;
+    auto factors = [&]() {
+#pragma unroll
+      for (int e = 0; e < EPV; ++e) {
+        up[e] = (kn >> e & 1) ? inv_rho : 1.f;
+        down[e] = (kn >> e & 1) ? rho : 1.f;
+      }
+    };
+    each<kAhead>([&](auto d) { load(raw[d], bits[d]); });
+    for (int it = 0; it < items; it += kAhead) {
+      each<kAhead>([&](auto d) {
+        if (it + d < items) {
+          const int e0 = (u * kThreads + tid) * EPV, v = v0 + u * kThreads + tid;
+          const int64_t row = start + j0 + j;
+          if constexpr (STATE) {
+            if (j == 0) {
+#pragma unroll
+              for (int e = 0; e < EPV; ++e) s[e] = sub[e0 + e];
+              kn = (uint32_t)(known[e0 >> 6] >> (e0 & 63));
+              co = (uint32_t)(counted[e0 >> 6] >> (e0 & 63));
+              factors();
+            } else {  // the previous row's proposal is part of the output from here on
+              const int tok = __builtin_amdgcn_readlane(lane_tok, j);
+              if (tok >= 0 && tok < P.vocab && tok / EPV == v) {
+#pragma unroll
+                for (int e = 0; e < EPV; ++e)
+                  if (tok % EPV == e) {
+                    s[e] += freq + ((co >> e & 1) ? 0.f : pres);
+                    co |= 1u << e;
+                    kn |= 1u << e;
+                  }
+                factors();
+              }
+            }
+          }
+          float x[EPV];
+          V::unpack(raw[d], x);
+          if constexpr (STATE) {
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) x[e] = __builtin_fmaf(x[e], x[e] > 0.f ? up[e] : down[e], -s[e]);
+          }
+          if (P.mask && __builtin_amdgcn_readlane(lane_mask, j) >= 0) {
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) x[e] = (bits[d] >> e & 1) ? x[e] : P.masked_value;
+          }
+          uint8_t* o = P.out + row * P.ld_out_bytes;
+          // (whole vectors of the tile; a row's last elements one by one)
+          const RowBuf out = row_buf(o + (int64_t)v0 * 16, (uint32_t)min(nv, P.vocab / EPV - v0) * 16u);
+          buf_store16_nt(out, (uint32_t)(u * kThreads + tid) * 16u, V::pack(x));
+          const int valid = P.vocab - v * EPV;
+          if (u * kThreads + tid < nv && valid < EPV) {
+#pragma unroll
+            for (int e = 0; e < EPV; ++e)
+              if (e < valid) V::put(o, v * EPV + e, x[e]);
+          }
+          if (++j == rows) {
+            j = 0;
+            ++u;
+          }
+          load(raw[d], bits[d]);
+        }
+      });
     }
   }
   if (blockIdx.x == 0) {  // one tile sees every list whole
@@ -199,12 +270,18 @@ __global__ void __launch_bounds__(kThreads) k_adjust(AdjustParams P) {
 }  // namespace
 
 hipError_t launch_adjust(const AdjustParams& p, int in_bf16, hipStream_t s) {
-  const int tiles = (p.nvec + kTileVec - 1) / kTileVec + (p.mask ? 1 : 0);
   // row groups of a block of average length, one for each layer of the grid
   int64_t z = (p.n_rows + (int64_t)p.n_blocks * kRowGroup - 1) / ((int64_t)p.n_blocks * kRowGroup);
   z = z < 1 ? 1 : z > 4096 ? 4096 : z;
+  // smaller tiles where the blocks are too few to fill the device
+  int tile = kTileVec;
+  while (tile > kThreads && (int64_t)p.n_blocks * z * ((p.nvec + tile - 1) / tile) < 1024) tile /= 2;
+  const int tiles = (p.nvec + tile - 1) / tile;
+  const bool state = p.history || p.draft || p.bias_tokens;
   for (int b0 = 0; b0 < p.n_blocks; b0 += 65535) {  // the grid's second dimension ends there
     AdjustParams q = p;
+    q.tile_vec = tile;
+    q.tiles = tiles;
     q.n_blocks = p.n_blocks - b0 < 65535 ? p.n_blocks - b0 : 65535;
     q.offsets += b0;
     if (q.history) q.history += (int64_t)b0 * p.ld_history;
@@ -216,11 +293,15 @@ hipError_t launch_adjust(const AdjustParams& p, int in_bf16, hipStream_t s) {
     if (q.bias_tokens) q.bias_tokens += (int64_t)b0 * p.ld_bias;
     if (q.bias_values) q.bias_values += (int64_t)b0 * p.ld_bias;
     if (q.bias_len) q.bias_len += b0;
-    const dim3 grid((unsigned)tiles, (unsigned)q.n_blocks, (unsigned)z);
-    if (in_bf16)
-      hipLaunchKernelGGL(k_adjust<true>, grid, dim3(kThreads), 0, s, q);
+    const dim3 grid((unsigned)(tiles + (p.mask ? 1 : 0)), (unsigned)q.n_blocks, (unsigned)z);
+    if (in_bf16 && state)
+      hipLaunchKernelGGL((k_adjust<true, true>), grid, dim3(kThreads), 0, s, q);
+    else if (in_bf16)
+      hipLaunchKernelGGL((k_adjust<true, false>), grid, dim3(kThreads), 0, s, q);
+    else if (state)
+      hipLaunchKernelGGL((k_adjust<false, true>), grid, dim3(kThreads), 0, s, q);
     else
-      hipLaunchKernelGGL(k_adjust<false>, grid, dim3(kThreads), 0, s, q);
+      hipLaunchKernelGGL((k_adjust<false, false>), grid, dim3(kThreads), 0, s, q);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -171,6 +171,8 @@ struct AdjustParams {
   int32_t n_masks;
   const int32_t* mask_row;
   float masked_value;
+  int32_t tile_vec;  // vectors of a row that a workgroup takes; tiles of a row (set by the launch)
+  int32_t tiles;
   uint32_t* flags;
 };
 

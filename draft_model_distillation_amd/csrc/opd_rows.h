@@ -5,9 +5,29 @@
 
 #include <stdint.h>
 
+#include <utility>
+
 #include <hip/hip_runtime.h>
 
 namespace opd {
+
+// f(0), f(1), .. f(N - 1) with constants, written out: what loops over an array of registers have to be
+// before the optimiser starts, or it may keep the array in one piece and copy it about.
+template <class F, int... I>
+__device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F&& f) {
+  each_of(f, std::make_integer_sequence<int, N>{});
+}
+
+// Indices from the hardware registers. (HIP's threadIdx and blockIdx are calls into the device library where
+// the IEEE mode is off, as it does not match the library's, and a workgroup's index that comes out of a call
+// is no longer known to be the same in every lane.)
+__device__ __forceinline__ int thread_x() { return (int)__builtin_amdgcn_workitem_id_x(); }
+__device__ __forceinline__ int group_x() { return (int)__builtin_amdgcn_workgroup_id_x(); }
+__device__ __forceinline__ int group_y() { return (int)__builtin_amdgcn_workgroup_id_y(); }
 
 constexpr float kLog2e = 1.44269504088896340736f;  // rounded to fp32; its multiples are exponents of 2
 constexpr float kNegInf = -__builtin_inff();
@@ -60,6 +80,12 @@ __device__ __forceinline__ uint32_t bf16_bits(float f) {
   return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f);
 }
 
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+
 // 16 bytes of logits as EPV floats and back (bf16 -> fp32 is exact).
 template <bool BF16>
 struct Vec;
@@ -77,8 +103,18 @@ struct Vec<true> {
   __device__ __forceinline__ static u32x4 pack(const float (&x)[8]) {
     u32x4 v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = bf16_bits(x[2 * i]) | (bf16_bits(x[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) v[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
     return v;
+  }
+  // The larger of m and a vector's elements, up to bits that max_value() takes off: a word of two elements
+  // is, as an fp32 number, its upper element with more digits.
+  __device__ __forceinline__ static float max(u32x4 v, float m) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(fmaxf(m, __uint_as_float(v[i])), __uint_as_float(v[i] << 16));
+    return m;
+  }
+  __device__ __forceinline__ static float max_value(float m) {
+    return __uint_as_float(__float_as_uint(m) & 0xffff0000u);
   }
   __device__ __forceinline__ static float elem(const uint8_t* row, int i) {
     return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << 16);
@@ -101,6 +137,12 @@ struct Vec<false> {
     for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(x[i]);
     return v;
   }
+  __device__ __forceinline__ static float max(u32x4 v, float m) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, __uint_as_float(v[i]));
+    return m;
+  }
+  __device__ __forceinline__ static float max_value(float m) { return m; }
   __device__ __forceinline__ static float elem(const uint8_t* row, int i) {
     return reinterpret_cast<const float*>(row)[i];
   }

@@ -4,12 +4,13 @@
 // Its first vectors are loaded into registers at once; the k-th largest of the maxima of groups of
 // threads over them is a lower bound of the k-th largest logit. From there on an element at or above the
 // bound is a candidate and goes, as a 64-bit key (value's order in the upper half, falling index in the
-// lower, so that no two are the same), into a buffer in LDS, and any other adds 2^(x log2 e - ref) to its
-// thread's sum; what is not in registers is streamed past the same bound. Where the whole row is held
-// (a bf16 row of 151,936 logits is), candidates are little more than k. They are ranked by counting, the
-// k largest are the answer, and the others join the sums in the order of their rank. The sum of the
-// others is never formed by subtracting the listed ones, which would lose what is left where the list
-// holds nearly all of the row.
+// lower, so that no two are the same), into a buffer in LDS, and any other adds 2^((x - bound) log2 e) to
+// its thread's sum; what is not in registers is streamed past the same bound. Candidates are few (for
+// random order k times the segment's length over the held part's). They are ranked by counting, the k
+// largest are the answer, and the others join the sums in the order of their rank. The sum of the others
+// is never formed by subtracting the listed ones, which would lose what is left where the list holds
+// nearly all of the row; where the bound turns out to be no reference for it (all others so far below
+// that their terms vanish), the segment is gone over once more for the sum alone.
 //
 // When the buffer would run over (rows of equal values; rising rows), it is cut to the k largest and the
 // bound raised to the k-th, after every few vectors if need be. Every set and every order of additions
@@ -45,24 +46,38 @@ __device__ __forceinline__ uint64_t make_key(float x, int index) {
   return ((uint64_t)order_key(x) << 32) | (uint32_t)~index;
 }
 
-// A thread's share of the log-sum-exp of the elements that are not listed: sum * 2^ref. The reference
-// may lag the largest exponent by up to 24: 2^24 an element leaves fp32 range to spare.
+// A thread's share of a log-sum-exp: sum * 2^ref. The reference may lag the largest exponent by up to
+// 24: 2^24 an element leaves fp32 range to spare.
 struct Rest {
   float ref = kNoRef, sum = 0.f;
-  __device__ __forceinline__ void raise(float m) {
-    const float c = m * kLog2e;
-    if (__builtin_amdgcn_ballot_w64(c > ref + 24.f)) {  // (a branch: it is hardly ever taken)
-      const float r = c > ref + 24.f ? c : ref;
-      sum *= ex2(ref - r);
-      ref = r;
+  __device__ __forceinline__ void add(float x) {
+    const float c = x * kLog2e;
+    if (c > ref + 24.f) {
+      sum *= ex2(ref - c);
+      ref = c;
     }
+    sum += ex2(__builtin_fmaf(x, kLog2e, -ref));
   }
-  __device__ __forceinline__ float term(float x) const { return ex2(__builtin_fmaf(x, kLog2e, -ref)); }
+};
+
+// The bound: elements at or above it are candidates. Once the buffer has been cut to k it is the next
+// number above the k-th: k keys above that are held, and the index of an element equal to the k-th that
+// comes later is higher than theirs.
+__device__ __forceinline__ float bound_after_cut(float kth) { return key_value(order_key(kth) + 1u); }
+
+// The sum of a thread's elements that were no candidates, relative to the bound (none is above it).
+struct Low {
+  float ref, sum = 0.f;
+  __device__ __forceinline__ void rebase(float bound) {
+    const float r = fmaxf(bound * kLog2e, kNoRef);
+    sum *= ex2(ref - r);
+    ref = r;
+  }
 };
 
 // Ends the arithmetic of a vector here: the compiler would otherwise keep vectors in unpacked form and put
 // their sums off together, which costs the registers that the row needs.
-__device__ __forceinline__ void settle(u32x4& v, Rest& r) { asm volatile("" : "+v"(v), "+v"(r.sum), "+v"(r.ref)); }
+__device__ __forceinline__ void settle(u32x4& v, Low& low) { asm volatile("" : "+v"(v), "+v"(low.sum)); }
 
 struct Shared {
   uint64_t keys[kTopkCap];
@@ -77,7 +92,7 @@ struct Shared {
 // its upper `bits` bits say, rounded down; -inf where there are not k.
 template <int M>
 __device__ void find_bound(Shared& S, int k, int bits) {
-  const int lane = threadIdx.x & 63;
+  const int lane = thread_x() & 63;
   uint32_t key[M / 64];
 #pragma unroll
   for (int i = 0; i < M / 64; ++i) key[i] = S.maxima[i * 64 + lane];
@@ -97,7 +112,7 @@ __device__ void find_bound(Shared& S, int k, int bits) {
 // threads call it.
 template <int T>
 __device__ int cut(Shared& S, int n, int k, Rest& rest) {
-  const int tid = threadIdx.x;
+  const int tid = thread_x();
   const uint64_t* from = S.keys;
   if (n <= kRankMost) {
     for (int i = tid; i < n; i += T) {
@@ -126,15 +141,7 @@ __device__ int cut(Shared& S, int n, int k, Rest& rest) {
         lds_barrier();
       }
   }
-  for (int i = k + tid; i < n; i += T) {
-    const float x = key_value((uint32_t)(from[i] >> 32));
-    const float c = x * kLog2e;
-    if (c > rest.ref + 24.f) {
-      rest.sum *= ex2(rest.ref - c);
-      rest.ref = c;
-    }
-    rest.sum += rest.term(x);
-  }
+  for (int i = k + tid; i < n; i += T) rest.add(key_value((uint32_t)(from[i] >> 32)));
   const int kept = min(n, k);
   if (from != S.keys)
     for (int i = tid; i < kept; i += T) S.keys[i] = from[i];
@@ -149,7 +156,7 @@ __device__ int cut(Shared& S, int n, int k, Rest& rest) {
 // Joins the threads' sums; the first wave has the result.
 template <int T>
 __device__ void join_rest(Shared& S, Rest& rest) {
-  const int tid = threadIdx.x;
+  const int tid = thread_x();
   wave_lse(rest.ref, rest.sum);
   if ((tid & 63) == 0) {
     S.pair[tid >> 6][0] = rest.ref;
@@ -166,83 +173,72 @@ __device__ void join_rest(Shared& S, Rest& rest) {
 // Writes a row's answer: the first `kept` keys (an entry that is not there: index -1) and the sum.
 template <int T>
 __device__ void write_row(const TopkParams& P, const Shared& S, int row, int kept, const Rest& rest) {
-  for (int i = threadIdx.x; i < P.k; i += T) {
+  for (int i = thread_x(); i < P.k; i += T) {
     const uint64_t key = i < kept ? S.keys[i] : 0;
     P.values[(int64_t)row * P.k + i] = key ? key_value((uint32_t)(key >> 32)) : kNegInf;
     P.index[(int64_t)row * P.k + i] = key ? (int32_t)~(uint32_t)key : -1;
   }
-  if (threadIdx.x == 0)  // the exponents are of fp32's log2(e), so that one is divided out
+  if (thread_x() == 0)  // the exponents are of fp32's log2(e), so that one is divided out
     P.rest_lse[row] = rest.sum > 0.f
                           ? (float)(((double)rest.ref + (double)lg2(rest.sum)) / (double)kLog2e)
                           : kNegInf;
 }
 
-// What a workgroup knows while it goes over its segment. Until the buffer has once been cut to k, an
-// element equal to the bound may belong to the list; from then on it cannot: k keys at or above the
-// bound are held, and its index is higher than theirs.
-struct Bound {
-  float at;
-  bool strict;
-  __device__ __forceinline__ bool above(float x) const { return strict ? x > at : x >= at; }
-};
-
-// One vector: candidates into the buffer, the others into the sum.
-template <int EPV>
-__device__ __forceinline__ void take(Shared& S, const Bound& B, Rest& rest, const float (&x)[EPV], int first, int end) {
+// One vector: candidates into the buffer, the others into the sum. The few lanes with candidates are taken
+// one by one, the wave's first lanes trying one element each.
+template <bool BF16>
+__device__ __forceinline__ void take(Shared& S, float bound, Low& low, const u32x4& raw, float (&x)[Vec<BF16>::EPV],
+                                     int first, int end) {
+  using V = Vec<BF16>;
+  constexpr int EPV = V::EPV;
   float m = x[0];
 #pragma unroll
   for (int e = 1; e < EPV; ++e) m = fmaxf(m, x[e]);
-  if (__builtin_amdgcn_ballot_w64(m >= B.at)) {
-    float o = kNegInf;  // the largest of those that are no candidates
-    float y[EPV];
+  uint64_t lanes = __builtin_amdgcn_ballot_w64(m >= bound);
+  if (lanes) {
+    const int lane = thread_x() & 63;
+    do {
+      const int from = __builtin_ctzll(lanes);
+      lanes &= lanes - 1;
+      uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < EPV; ++e) {
-      const bool cand = B.above(x[e]);
-      if (cand && first + e < end) {
-        const int at = atomicAdd(&S.count, 1);
-        if (at < kTopkCap) S.keys[at] = make_key(x[e], first + e);
+      for (int j = 0; j < 4; ++j) w[j] = (uint32_t)__builtin_amdgcn_readlane((int)raw[j], from);
+      const int at = __builtin_amdgcn_readlane(first, from) + lane;
+      const int j = BF16 ? lane >> 1 : lane;
+      const uint32_t word = j == 0 ? w[0] : j == 1 ? w[1] : j == 2 ? w[2] : w[3];
+      const float v = __uint_as_float(!BF16 || (lane & 1) ? word & (BF16 ? 0xffff0000u : ~0u) : word << 16);
+      if (lane < EPV && v >= bound && at < end) {
+        const int place = atomicAdd(&S.count, 1);
+        if (place < kTopkCap) S.keys[place] = make_key(v, at);
       }
-      y[e] = cand ? kNegInf : x[e];
-      o = fmaxf(o, y[e]);
-    }
-    rest.raise(o);
-    float s = 0.f;
+    } while (lanes);
 #pragma unroll
-    for (int e = 0; e < EPV; ++e) s += rest.term(y[e]);
-    rest.sum += s;
-  } else {
-    rest.raise(m);
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < EPV; ++e) s += rest.term(x[e]);
-    rest.sum += s;
+    for (int e = 0; e < EPV; ++e) x[e] = x[e] >= bound ? kNegInf : x[e];
   }
+  float s = 0.f;
+#pragma unroll
+  for (int e = 0; e < EPV; ++e) s += ex2(__builtin_fmaf(x[e], kLog2e, -low.ref));
+  low.sum += s;
 }
 
 // The candidates of one vector per thread again, in batches of threads, cutting the buffer before it could
 // run over (`was`: the bound that take() went by; the others are in the sum already). All threads.
 template <int EPV, int T>
-__device__ void take_again(Shared& S, Bound& B, const Bound& was, Rest& rest, const float (&x)[EPV], int first, int end,
+__device__ void take_again(Shared& S, float& bound, float was, Rest& rest, const float (&x)[EPV], int first, int end,
                            int& n, int k) {
   for (int b = 0; b < T / kBatch; ++b) {
     if (n + kBatch * EPV > kTopkCap) {
       n = cut<T>(S, n, k, rest);
-      if (n == k) B = Bound{S.bound, true};
+      if (n == k) bound = bound_after_cut(S.bound);
     }
-    if ((int)threadIdx.x / kBatch == b) {
+    if (thread_x() / kBatch == b) {
 #pragma unroll
       for (int e = 0; e < EPV; ++e)
-        if (was.above(x[e]) && first + e < end) {
-          if (B.above(x[e])) {
+        if (x[e] >= was && first + e < end) {
+          if (x[e] >= bound)
             S.keys[atomicAdd(&S.count, 1)] = make_key(x[e], first + e);
-          } else {
-            const float c = x[e] * kLog2e;
-            if (c > rest.ref + 24.f) {
-              rest.sum *= ex2(rest.ref - c);
-              rest.ref = c;
-            }
-            rest.sum += rest.term(x[e]);
-          }
+          else
+            rest.add(x[e]);
         }
     }
     lds_barrier();
@@ -259,8 +255,8 @@ __global__ void __launch_bounds__(T) k_topk(TopkParams P) {
   constexpr int EPV = V::EPV;
   constexpr int U = kLoose;
   __shared__ Shared S;
-  const int tid = threadIdx.x;
-  const int row = blockIdx.x / P.n_seg, seg = blockIdx.x - row * P.n_seg;
+  const int tid = thread_x();
+  const int row = group_x(), seg = group_y();
   const int v0 = seg * P.seg_vec, n_vec = min(P.seg_vec, P.nvec - v0), k = P.k;
   const int base = v0 * EPV, end = min((v0 + n_vec) * EPV, P.vocab);  // tokens [base, end)
   const RowBuf in = row_buf(P.y + (int64_t)row * P.ld_bytes + (int64_t)v0 * 16, (uint32_t)n_vec * 16u);
@@ -282,95 +278,120 @@ __global__ void __launch_bounds__(T) k_topk(TopkParams P) {
 #pragma unroll
   for (int i = 0; i < H; ++i)
     if (i * T < n_vec) {
-      float x[EPV];
-      unpack(held[i], i * T, x);
+      if (base + (i * T + T) * EPV > end) {
+        float x[EPV];
+        unpack(held[i], i * T, x);
 #pragma unroll
-      for (int e = 0; e < EPV; ++e) m = fmaxf(m, x[e]);
+        for (int e = 0; e < EPV; ++e) m = fmaxf(m, x[e]);
+      } else {
+        m = V::max(held[i], m);
+      }
       asm volatile("" : "+v"(held[i]), "+v"(m));
     }
   {
     constexpr int G = T / M;  // threads per maximum: neighbours
-    float g = m;
-    if (G >= 2) g = fmaxf(g, __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(g), 0xB1, 0xF, 0xF, true)));
-    if (G >= 4) g = fmaxf(g, __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(g), 0x4E, 0xF, 0xF, true)));
     static_assert(G == 1 || G == 2 || G == 4, "maxima of one, two or four lanes");
+    float g = V::max_value(m);
+    if (G >= 2) g = fmaxf(g, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(g), 0xB1, 0xF, 0xF, true)));
+    if (G >= 4) g = fmaxf(g, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(g), 0x4E, 0xF, 0xF, true)));
     // (-inf is also what a group without elements has: no maximum, so that fewer than k of them are seen)
     if (tid % G == 0) S.maxima[tid / G] = g > kNegInf ? order_key(g) : 0u;
   }
   lds_barrier();
   if (tid < 64) find_bound<M>(S, k, BF16 ? 16 : 24);
   lds_barrier();
-  Bound B{S.bound, false};
-  int n = 0;
+  float bound = S.bound;
   Rest rest;
-  rest.ref = m > kNegInf && m < B.at ? m * kLog2e : kNoRef;  // no candidate among the thread's: m is its largest
+  Low low;
+  low.ref = fmaxf(bound * kLog2e, kNoRef);
 #pragma unroll
   for (int i = 0; i < H; ++i)
     if (i * T < n_vec) {
       float x[EPV];
       unpack(held[i], i * T, x);
-      take<EPV>(S, B, rest, x, base + (i * T + tid) * EPV, end);
-      settle(held[i], rest);
+      take<BF16>(S, bound, low, held[i], x, base + (i * T + tid) * EPV, end);
+      settle(held[i], low);
     }
-  lds_barrier();
-  n = S.count;
-  lds_barrier();
-  if (n > kTopkCap) {
-    if (tid == 0) S.count = 0;
-    lds_barrier();
-    n = 0;
-    const Bound was = B;
-#pragma unroll 1
-    for (int i = 0; i * T < n_vec && i < H; ++i) {
-      // (read again: held[i] with i not a constant would put the row into memory)
-      u32x4 raw = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)(i * T) * 16u);
-      float x[EPV];
-      unpack(raw, i * T, x);
-      take_again<EPV, T>(S, B, was, rest, x, base + (i * T + tid) * EPV, end, n, k);
-    }
-  }
-  for (int g0 = H * T; g0 < n_vec; g0 += U * T) {
-    u32x4 raw[U];
+  // What has been gone over ends at vector g1: the held ones, then U per thread at a time.
+  int n = 0, g0 = 0, g1 = H * T;
+  for (;;) {
+    if (g0 > 0) {
+      u32x4 raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) raw[u] = buf_load16<kStream>(in, (uint32_t)tid * 16u, (uint32_t)(g0 + u * T) * 16u);
-    if (n > kTopkCap / 4) {
-      n = cut<T>(S, n, k, rest);
-      if (n == k) B = Bound{S.bound, true};
-    }
+      for (int u = 0; u < U; ++u) raw[u] = buf_load16<kStream>(in, (uint32_t)tid * 16u, (uint32_t)(g0 + u * T) * 16u);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float x[EPV];
-      unpack(raw[u], g0 + u * T, x);
-      take<EPV>(S, B, rest, x, base + (g0 + u * T + tid) * EPV, end);
-      settle(raw[u], rest);
+      for (int u = 0; u < U; ++u) {
+        float x[EPV];
+        unpack(raw[u], g0 + u * T, x);
+        take<BF16>(S, bound, low, raw[u], x, base + (g0 + u * T + tid) * EPV, end);
+        settle(raw[u], low);
+      }
     }
+    const bool last = g1 >= n_vec;
     lds_barrier();
     const int total = S.count;
     lds_barrier();
     if (total <= kTopkCap) {
       n = total;
-      continue;
+    } else {
+      // more candidates than places: back to the keys of before, and those vectors again
+      if (tid == 0) S.count = n;
+      lds_barrier();
+      const float was = bound;
+      for (int v = g0; v < g1 && v < n_vec; v += T) {
+        u32x4 raw = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)v * 16u);
+        float x[EPV];
+        unpack(raw, v, x);
+        take_again<EPV, T>(S, bound, was, rest, x, base + (v + tid) * EPV, end, n, k);
+      }
+      low.rebase(bound);
     }
-    if (tid == 0) S.count = n;
-    lds_barrier();
-    const Bound was = B;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float x[EPV];
-      unpack(raw[u], g0 + u * T, x);
-      take_again<EPV, T>(S, B, was, rest, x, base + (g0 + u * T + tid) * EPV, end, n, k);
+    if (last) break;
+    if (n > kTopkCap / 4) {
+      n = cut<T>(S, n, k, rest);
+      if (n == k) bound = bound_after_cut(S.bound);
+      low.rebase(bound);
     }
+    g0 = g1;
+    g1 += U * T;
   }
   const int kept = cut<T>(S, n, k, rest);
+  // The bound was a reference for the sum if the terms add up to something (2^-40 of the bound's own
+  // leaves those below fp32's smallest number 2^86 times less); else the others again, by themselves.
+  {
+    float t = wave_sum(low.sum);
+    if ((tid & 63) == 0) S.pair[tid >> 6][0] = t;
+    lds_barrier();
+    t = 0.f;
+    for (int w = 0; w < T / 64; ++w) t += S.pair[w][0];
+    lds_barrier();
+    if (t >= 0x1p-40f) {
+      lse_join(rest.ref, rest.sum, low.ref, low.sum);
+    } else {
+      rest = Rest{};
+      const uint64_t least = kept == k ? S.keys[k - 1] : 0;
+      for (int v = 0; v < n_vec; v += T) {
+        u32x4 raw = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)v * 16u);
+        float x[EPV];
+        unpack(raw, v, x);
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) {
+          const int i = base + (v + tid) * EPV + e;
+          if (i < end && make_key(x[e], i) < least) rest.add(x[e]);
+        }
+      }
+    }
+  }
   join_rest<T>(S, rest);
   if (P.n_seg == 1) {
     write_row<T>(P, S, row, kept, rest);
   } else {
-    uint64_t* keys = P.seg_keys + (int64_t)blockIdx.x * k;
+    const int64_t unit = (int64_t)row * P.n_seg + seg;
+    uint64_t* keys = P.seg_keys + unit * k;
     for (int i = tid; i < k; i += T) keys[i] = i < kept ? S.keys[i] : 0;
     if (tid == 0) {
-      P.seg_lse[2 * (int64_t)blockIdx.x] = rest.ref;
-      P.seg_lse[2 * (int64_t)blockIdx.x + 1] = rest.sum;
+      P.seg_lse[2 * unit] = rest.ref;
+      P.seg_lse[2 * unit + 1] = rest.sum;
     }
   }
 }
@@ -380,7 +401,7 @@ __global__ void __launch_bounds__(T) k_topk(TopkParams P) {
 __global__ void __launch_bounds__(kThreads) k_topk_merge(TopkParams P) {
   constexpr int T = kThreads, R = kTopkCap / T;
   __shared__ Shared S;
-  const int tid = threadIdx.x, row = blockIdx.x, k = P.k;
+  const int tid = thread_x(), row = group_x(), k = P.k;
   const int total = P.n_seg * k;
   const uint64_t* keys = P.seg_keys + (int64_t)row * total;
   uint64_t mine[R];
@@ -405,16 +426,10 @@ __global__ void __launch_bounds__(kThreads) k_topk_merge(TopkParams P) {
   for (int i = 0; i < R; ++i) {
     if (mine[i] == 0) continue;  // (a list that was not full)
     const float x = key_value((uint32_t)(mine[i] >> 32));
-    if (x >= bound) {
+    if (x >= bound)
       S.keys[atomicAdd(&S.count, 1)] = mine[i];
-    } else {
-      const float c = x * kLog2e;
-      if (c > rest.ref + 24.f) {
-        rest.sum *= ex2(rest.ref - c);
-        rest.ref = c;
-      }
-      rest.sum += rest.term(x);
-    }
+    else
+      rest.add(x);
   }
   lds_barrier();
   const int kept = cut<T>(S, S.count, k, rest);
@@ -426,7 +441,7 @@ constexpr int kWholeRows = 192;  // rows from which a workgroup per row is faste
 
 template <bool BF16, int T, int H, int M>
 hipError_t launch(const TopkParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((k_topk<BF16, T, H, M>), dim3((unsigned)((int64_t)p.n_rows * p.n_seg)), dim3(T), 0, s, p);
+  hipLaunchKernelGGL((k_topk<BF16, T, H, M>), dim3((unsigned)p.n_rows, (unsigned)p.n_seg), dim3(T), 0, s, p);
   return hipGetLastError();
 }
 
@@ -434,7 +449,8 @@ template <bool BF16>
 hipError_t launch_rows(const TopkParams& p, hipStream_t s) {
   if (p.seg_vec <= 256 * 8) return launch<BF16, 256, 8, 256>(p, s);
   if (p.seg_vec <= 512 * 10) return launch<BF16, 512, 10, 512>(p, s);
-  return p.k <= 96 ? launch<BF16, 1024, 19, 256>(p, s) : launch<BF16, 1024, 19, 512>(p, s);
+  if (p.n_rows < 512) return p.k <= 96 ? launch<BF16, 1024, 19, 256>(p, s) : launch<BF16, 1024, 19, 512>(p, s);
+  return p.k <= 96 ? launch<BF16, 512, 12, 256>(p, s) : launch<BF16, 512, 12, 512>(p, s);
 }
 
 }  // namespace

@@ -67,7 +67,7 @@ __host__ __device__ inline int bitmap_words(int n, int epv) { return (n * epv + 
 // whole row's bitmap (cleared before). Loads of z are left in flight.
 template <bool BF16>
 __device__ void read_list(const TopkLossParams& P, ClassShared& S, uint32_t* listed, int row, bool report, List& li) {
-  const int lane = threadIdx.x & 63;
+  const int lane = thread_x() & 63;
   const uint8_t* zr = P.z + (int64_t)row * P.ld_bytes;
   bool clash = false, bad = false;
 #pragma unroll
@@ -126,7 +126,7 @@ struct Dist {
 };
 __device__ __forceinline__ void distribution(const float (&x)[kSlots], float x_max, int owner, float ref, float l2,
                                              Dist& D) {
-  const int lane = threadIdx.x & 63;
+  const int lane = thread_x() & 63;
   const float above = __builtin_fmaf(x_max, kLog2e, -ref);  // of the largest listed, relative to ref
   const bool rest_top = l2 > above;
   D.top = rest_top ? -1 : owner;
@@ -148,7 +148,7 @@ __device__ __forceinline__ void distribution(const float (&x)[kSlots], float x_m
 // memory. (ref, sum): the tokens that are not listed.
 __device__ void row_classes(const TopkLossParams& P, ClassShared& S, int row, const List& li, float ref, float l2,
                             bool write) {
-  const int lane = threadIdx.x & 63;
+  const int lane = thread_x() & 63;
   const float inf = __builtin_inff();
   float t_max = kNegInf, z_max = kNegInf;
 #pragma unroll
@@ -275,7 +275,7 @@ __device__ __forceinline__ void settle(u32x4& v, Rest& r) { asm volatile("" : "+
 template <int EPV, int T>
 __device__ __forceinline__ void clear_bitmap(uint32_t* listed, int v0, int n, int end) {
   const int words = bitmap_words(n, EPV), t0 = v0 * EPV;
-  for (int w = threadIdx.x; w < words; w += T) {
+  for (int w = thread_x(); w < words; w += T) {
     const int left = end - t0 - 32 * w;
     listed[w] = left >= 32 ? 0u : left <= 0 ? ~0u : ~0u << left;
   }
@@ -297,7 +297,7 @@ __device__ __forceinline__ void grad_vector(const RowBuf& out, int tid, int v, u
     buf_store16_nt(out, at + 16, Vec<false>::pack({x[4], x[5], x[6], x[7]}));
   } else if constexpr (!BF16 && OUT_BF16) {
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    const u32x2 w = {bf16_bits(x[0]) | (bf16_bits(x[1]) << 16), bf16_bits(x[2]) | (bf16_bits(x[3]) << 16)};
+    const u32x2 w = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
     __builtin_amdgcn_raw_buffer_store_b64(w, out.r, (int)at, 0, kStream);
   } else {
     buf_store16_nt(out, at, V::pack(x));
@@ -307,7 +307,7 @@ __device__ __forceinline__ void grad_vector(const RowBuf& out, int tid, int v, u
 // The elements behind the row's last whole vector, one thread each.
 template <bool BF16, bool OUT_BF16>
 __device__ __forceinline__ void grad_tail(const TopkLossParams& P, const uint8_t* zr, uint8_t* dr, float L, float factor) {
-  const int i = P.vocab / Vec<BF16>::EPV * Vec<BF16>::EPV + (int)threadIdx.x;
+  const int i = P.vocab / Vec<BF16>::EPV * Vec<BF16>::EPV + thread_x();
   if (i < P.vocab) Vec<OUT_BF16>::put(dr, i, factor * ex2(__builtin_fmaf(Vec<BF16>::elem(zr, i), kLog2e, -L)));
 }
 
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(T) k_topk_loss_hold(TopkLossParams P) {
   constexpr int U = kLoose;
   __shared__ ClassShared S;
   extern __shared__ uint32_t listed[];
-  const int tid = threadIdx.x, row = blockIdx.x;
+  const int tid = thread_x(), row = group_x();
   const uint8_t* zr = P.z + (int64_t)row * P.ld_bytes;
   const int nvec = P.nvec;
   const RowBuf in = row_buf(zr, (uint32_t)nvec * 16u);
@@ -405,8 +405,8 @@ __global__ void __launch_bounds__(kThreads) k_topk_loss_sums(TopkLossParams P) {
   constexpr int EPV = V::EPV;
   __shared__ float part[kThreads / 64][2];
   __shared__ uint32_t listed[kSegVec * EPV / 32];
-  const int tid = threadIdx.x;
-  const int row = blockIdx.x / P.n_seg, seg = blockIdx.x - row * P.n_seg;
+  const int tid = thread_x();
+  const int row = group_x(), seg = group_y();
   const uint8_t* zr = P.z + (int64_t)row * P.ld_bytes;
   const int v0 = seg * P.seg_vec, v1 = min(v0 + P.seg_vec, P.nvec);
   const RowBuf in = row_buf(zr, (uint32_t)v1 * 16u);
@@ -438,8 +438,9 @@ __global__ void __launch_bounds__(kThreads) k_topk_loss_sums(TopkLossParams P) {
   if (tid == 0) {
     float ref = part[0][0], sum = part[0][1];
     for (int w = 1; w < kThreads / 64; ++w) lse_join(ref, sum, part[w][0], part[w][1]);
-    P.seg_lse[2 * (int64_t)blockIdx.x] = ref;
-    P.seg_lse[2 * (int64_t)blockIdx.x + 1] = sum;
+    float* p = P.seg_lse + 2 * ((int64_t)row * P.n_seg + seg);
+    p[0] = ref;
+    p[1] = sum;
   }
 }
 
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(kThreads) k_topk_loss_sums(TopkLossParams P) {
 __device__ void join_segments(const TopkLossParams& P, int row, float& ref, float& l2) {
   float sum = 0.f;
   ref = kNoRef;
-  for (int i = threadIdx.x & 63; i < P.n_seg; i += 64) {
+  for (int i = thread_x() & 63; i < P.n_seg; i += 64) {
     const float* p = P.seg_lse + 2 * ((int64_t)row * P.n_seg + i);
     lse_join(ref, sum, p[0], p[1]);
   }
@@ -460,7 +461,7 @@ template <bool BF16>
 __global__ void __launch_bounds__(64) k_topk_loss_row(TopkLossParams P) {
   __shared__ ClassShared S;
   extern __shared__ uint32_t listed[];
-  const int row = blockIdx.x;
+  const int row = group_x();
   clear_bitmap<Vec<BF16>::EPV, 64>(listed, 0, P.nvec, P.vocab);
   lds_barrier();
   List li;
@@ -478,8 +479,8 @@ __global__ void __launch_bounds__(kThreads) k_topk_loss_grad(TopkLossParams P) {
   constexpr int EPV = V::EPV;
   __shared__ ClassShared S;
   extern __shared__ uint32_t listed[];
-  const int tid = threadIdx.x;
-  const int row = blockIdx.x / P.n_seg, seg = blockIdx.x - row * P.n_seg;
+  const int tid = thread_x();
+  const int row = group_x(), seg = group_y();
   const uint8_t* zr = P.z + (int64_t)row * P.ld_bytes;
   uint8_t* dr = P.dz + (int64_t)row * P.ld_dz_bytes;
   const int v0 = seg * P.seg_vec, v1 = min(v0 + P.seg_vec, P.nvec);
@@ -523,7 +524,7 @@ constexpr int kHoldRows = 128;  // rows from which a workgroup per row is faster
 // Launches a kernel with a row's bitmap in LDS (above 64 KiB with the kernel's own for the widest rows,
 // which has to be allowed; the setting is per device, so it is made on every such launch).
 template <class K>
-hipError_t launch_with_bitmap(K kernel, int64_t grid, int threads, int vectors, int epv, const TopkLossParams& p,
+hipError_t launch_with_bitmap(K kernel, dim3 grid, int threads, int vectors, int epv, const TopkLossParams& p,
                               hipStream_t s) {
   const size_t lds = 4 * (size_t)bitmap_words(vectors, epv);
   if (lds + sizeof(ClassShared) > 64 * 1024) {
@@ -531,26 +532,25 @@ hipError_t launch_with_bitmap(K kernel, int64_t grid, int threads, int vectors, 
         hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3((unsigned)threads), lds, s, p);
+  hipLaunchKernelGGL(kernel, grid, dim3((unsigned)threads), lds, s, p);
   return hipGetLastError();
 }
 
 template <bool BF16, bool OUT_BF16, bool GRAD, int T, int H>
 hipError_t launch_hold(const TopkLossParams& p, hipStream_t s) {
-  return launch_with_bitmap(k_topk_loss_hold<BF16, OUT_BF16, GRAD, T, H>, p.n_rows, T,
+  return launch_with_bitmap(k_topk_loss_hold<BF16, OUT_BF16, GRAD, T, H>, dim3((unsigned)p.n_rows), T,
                             hold_vectors<T, H, kLoose>(p.nvec), Vec<BF16>::EPV, p, s);
 }
 
 template <bool BF16, bool OUT_BF16, bool JOIN>
 hipError_t launch_grad(const TopkLossParams& p, hipStream_t s) {
-  return launch_with_bitmap(k_topk_loss_grad<BF16, OUT_BF16, JOIN>, (int64_t)p.n_rows * p.n_seg, kThreads, p.nvec,
+  return launch_with_bitmap(k_topk_loss_grad<BF16, OUT_BF16, JOIN>, dim3((unsigned)p.n_rows, (unsigned)p.n_seg), kThreads, p.nvec,
                             Vec<BF16>::EPV, p, s);
 }
 
 template <bool BF16>
 hipError_t launch_sums(const TopkLossParams& p, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)p.n_rows * p.n_seg));
-  hipLaunchKernelGGL(k_topk_loss_sums<BF16>, grid, dim3(kThreads), 0, s, p);
+  hipLaunchKernelGGL(k_topk_loss_sums<BF16>, dim3((unsigned)p.n_rows, (unsigned)p.n_seg), dim3(kThreads), 0, s, p);
   return hipGetLastError();
 }
 
@@ -570,7 +570,7 @@ hipError_t launch_fwd(const TopkLossParams& p, hipStream_t s) {
   if (p.n_rows >= kHoldRows) return launch_hold<BF16, false, false, 512, 0>(p, s);
   const hipError_t e = launch_sums<BF16>(p, s);
   if (e != hipSuccess) return e;
-  return launch_with_bitmap(k_topk_loss_row<BF16>, p.n_rows, 64, p.nvec, Vec<BF16>::EPV, p, s);
+  return launch_with_bitmap(k_topk_loss_row<BF16>, dim3((unsigned)p.n_rows), 64, p.nvec, Vec<BF16>::EPV, p, s);
 }
 
 }  // namespace
