@@ -7,8 +7,8 @@ built this module raises instead of computing anything another way.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -237,22 +237,28 @@ def _vector(t, name: str, n: int, dtype, optional: bool = False):
     if t is None:
         _require(optional, f"{name} is required")
         return
-    _require(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
-    _require(t.is_contiguous(), f"{name} must be contiguous")
-    _require(int(t.numel()) == int(n), f"{name} must have {n} elements, got {int(t.numel())}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got {int(t.numel())}")
 
 
 def _rows_matrix(t, name: str, rows: int, cols: int, dtype):
     """A contiguous [rows, cols] tensor of `dtype`."""
-    _require(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
-    _require(t.is_contiguous() and tuple(t.shape) == (rows, cols), f"{name} must be a contiguous [{rows}, {cols}] tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous() or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must be a contiguous [{rows}, {cols}] tensor")
 
 
 def _same_device(dev, named):
-    _require(dev.type == "cuda", f"tensors must be on a CUDA (HIP) device, got {dev}")
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA (HIP) device, got {dev}")
     for name, t in named:
-        if t is not None:
-            _require(t.device == dev, f"{name} is on {t.device}, expected {dev}")
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
 def _logit_pair(z, y):
@@ -324,10 +330,10 @@ def _ptr(t) -> Optional[int]:
 
 def _empty_rows(rows: int, vocab: int, dtype, device):
     """[rows, vocab] tensor whose row pitch is rounded up to 16 bytes (the library's alignment rule)."""
-    torch = _torch()
-    per = 16 // torch.empty((), dtype=dtype).element_size()
+    per = 16 // dtype.itemsize
     ld = ((vocab + per - 1) // per) * per
-    return torch.empty(rows, ld, dtype=dtype, device=device)[:, :vocab]
+    t = _torch().empty(rows, ld, dtype=dtype, device=device)
+    return t if ld == vocab else t[:, :vocab]
 
 
 _ws_cache = {}
@@ -748,12 +754,35 @@ def _table(t, name: str, rows: int, dtype):
     return int(t.shape[1]), int(t.stride(0)) if rows > 1 else int(max(t.stride(0), t.shape[1]))
 
 
-def _device_guard(dev):
-    """Launches go to the current device, which need not be the tensors'."""
-    torch = _torch()
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+def _on_device(f):
+    """Runs a call whose first tensor is on another device than the current one with that device current:
+    launches go to the current device."""
+
+    @functools.wraps(f)
+    def call(first, *args, **kw):
+        dev = first.device
+        if dev.type == "cuda" and dev.index != _torch().cuda.current_device():
+            with _torch().cuda.device(dev):
+                return f(first, *args, **kw)
+        return f(first, *args, **kw)
+
+    return call
 
 
+def _stream_and_workspace(dev, ws):
+    """The device's current stream (its handle) and the workspace to use on it."""
+    st = _torch().cuda.current_stream(dev)
+    handle = st.cuda_stream
+    if ws is None:
+        ws = _ws_cache.get((dev.type, dev.index, handle))
+        if ws is None:
+            ws = workspace(dev, st)
+    else:
+        _workspace_arg(ws, dev)
+    return handle, ws
+
+
+@_on_device
 def adjust_logits(x, offsets, history=None, history_len=None, prompt_len=None, draft_tokens=None, repetition=None,
                   frequency=None, presence=None, bias_tokens=None, bias_values=None, bias_len=None, mask=None,
                   mask_row=None, masked_value: float = -1.0e4, out=None, ws=None):
@@ -824,13 +853,11 @@ def adjust_logits(x, offsets, history=None, history_len=None, prompt_len=None, d
                        ("bias_values", bias_values), ("bias_len", bias_len), ("mask", mask), ("mask_row", mask_row),
                        ("out", out)])
     lib = load_library()
-    with _device_guard(dev):
-        ws = _workspace_arg(ws, dev)
-        if out is None:
-            out = _empty_rows(rows, vocab, x.dtype, dev)
-            op, _, _, ld_o = _matrix(out, "out", whole_vectors=False)
-        st = lib.opd_adjust_logits(xp, dt, rows, vocab, ld, ctypes.byref(a), op, ld_o, ws.data_ptr(), ws.numel(),
-                                   _stream(dev))
+    stream, ws = _stream_and_workspace(dev, ws)
+    if out is None:
+        out = _empty_rows(rows, vocab, x.dtype, dev)
+        op, ld_o = out.data_ptr(), out.stride(0)
+    st = lib.opd_adjust_logits(xp, dt, rows, vocab, ld, ctypes.byref(a), op, ld_o, ws.data_ptr(), ws.numel(), stream)
     _check("opd_adjust_logits", st)
     return out
 
@@ -846,6 +873,7 @@ def _nbytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
+@_on_device
 def topk_rows(y, k: int, scratch=None, ws=None, out=None) -> dict:
     """The k largest logits of every row and the log-sum-exp of its others (opd_topk_rows).
 
@@ -869,16 +897,14 @@ def topk_rows(y, k: int, scratch=None, ws=None, out=None) -> dict:
     dev = y.device
     _same_device(dev, [("scratch", scratch)] + [(n, o.get(n)) for n in ("values", "index", "rest_lse")])
     lib = load_library()
-    with _device_guard(dev):
-        ws = _workspace_arg(ws, dev)
-        scratch = _scratch_arg(scratch, lib.opd_topk_scratch_size(rows, vocab, dt, k), dev)
-        if not o:
-            o["values"] = torch.empty(rows, k, dtype=torch.float32, device=dev)
-            o["index"] = torch.empty(rows, k, dtype=torch.int32, device=dev)
-            o["rest_lse"] = torch.empty(rows, dtype=torch.float32, device=dev)
-        st = lib.opd_topk_rows(yp, dt, rows, vocab, ld, k, o["values"].data_ptr(), o["index"].data_ptr(),
-                               o["rest_lse"].data_ptr(), _ptr(scratch), _nbytes(scratch), ws.data_ptr(), ws.numel(),
-                               _stream(dev))
+    stream, ws = _stream_and_workspace(dev, ws)
+    scratch = _scratch_arg(scratch, lib.opd_topk_scratch_size(rows, vocab, dt, k), dev)
+    if not o:
+        o["values"] = torch.empty(rows, k, dtype=torch.float32, device=dev)
+        o["index"] = torch.empty(rows, k, dtype=torch.int32, device=dev)
+        o["rest_lse"] = torch.empty(rows, dtype=torch.float32, device=dev)
+    st = lib.opd_topk_rows(yp, dt, rows, vocab, ld, k, o["values"].data_ptr(), o["index"].data_ptr(),
+                           o["rest_lse"].data_ptr(), _ptr(scratch), _nbytes(scratch), ws.data_ptr(), ws.numel(), stream)
     _check("opd_topk_rows", st)
     return o
 
@@ -903,13 +929,15 @@ def _topk_loss_args(z, top_index, top_logit, rest_lse, alpha, tau, kl):
 
 
 def _dz_arg(dz, z, rows, vocab):
-    """Checks a caller's dz against z."""
+    """Checks a caller's dz against z; returns its pitch."""
     _dtype_code(dz)
-    _, rows_d, vocab_d, _ = _matrix(dz, "dz", whole_vectors=False)
+    _, rows_d, vocab_d, ld = _matrix(dz, "dz", whole_vectors=False)
     _require((rows_d, vocab_d) == (rows, vocab), f"dz must be [{rows}, {vocab}], got {tuple(dz.shape)}")
     _no_overlap(dz, z, "dz", "z")
+    return ld
 
 
+@_on_device
 def topk_loss_fwd(z, top_index, top_logit, rest_lse, alpha: float, tau: float, kl: str = "reverse", scratch=None,
                   ws=None):
     """Distillation loss against a teacher's top logits (opd_topk_loss_fwd).
@@ -924,17 +952,17 @@ def topk_loss_fwd(z, top_index, top_logit, rest_lse, alpha: float, tau: float, k
     dev = z.device
     _same_device(dev, lists + [("scratch", scratch)])
     lib = load_library()
-    with _device_guard(dev):
-        ws = _workspace_arg(ws, dev)
-        scratch = _scratch_arg(scratch, lib.opd_topk_loss_scratch_size(rows, vocab, args[1]), dev)
-        loss = torch.empty(rows, dtype=torch.float32, device=dev)
-        stats = torch.empty(rows, 4, dtype=torch.float32, device=dev)
-        st = lib.opd_topk_loss_fwd(*args, loss.data_ptr(), stats.data_ptr(), _ptr(scratch), _nbytes(scratch),
-                                   ws.data_ptr(), ws.numel(), _stream(dev))
+    stream, ws = _stream_and_workspace(dev, ws)
+    scratch = _scratch_arg(scratch, lib.opd_topk_loss_scratch_size(rows, vocab, args[1]), dev)
+    loss = torch.empty(rows, dtype=torch.float32, device=dev)
+    stats = torch.empty(rows, 4, dtype=torch.float32, device=dev)
+    st = lib.opd_topk_loss_fwd(*args, loss.data_ptr(), stats.data_ptr(), _ptr(scratch), _nbytes(scratch),
+                               ws.data_ptr(), ws.numel(), stream)
     _check("opd_topk_loss_fwd", st)
     return loss, stats
 
 
+@_on_device
 def topk_loss_bwd(z, top_index, top_logit, rest_lse, alpha: float, tau: float, row_stats, kl: str = "reverse",
                   grad_loss=None, dz_dtype=None, dz=None, ws=None):
     """Returns dz [R, V] (dz_dtype, default z.dtype) = grad_loss[row] * d loss_row / d z_row, from the
@@ -944,21 +972,21 @@ def topk_loss_bwd(z, top_index, top_logit, rest_lse, alpha: float, tau: float, r
     _rows_matrix(row_stats, "row_stats", rows, 4, torch.float32)
     _vector(grad_loss, "grad_loss", rows, torch.float32, optional=True)
     if dz is not None:
-        _dz_arg(dz, z, rows, vocab)
+        ld_dz = _dz_arg(dz, z, rows, vocab)
     dev = z.device
     _same_device(dev, lists + [("row_stats", row_stats), ("grad_loss", grad_loss), ("dz", dz)])
     lib = load_library()
-    with _device_guard(dev):
-        ws = _workspace_arg(ws, dev)
-        if dz is None:
-            dz = _empty_rows(rows, vocab, dz_dtype or z.dtype, dev)
-        dzp, _, _, ld_dz = _matrix(dz, "dz", whole_vectors=False)
-        st = lib.opd_topk_loss_bwd(*args, row_stats.data_ptr(), _ptr(grad_loss), dzp, _dtype_code(dz), ld_dz,
-                                   ws.data_ptr(), ws.numel(), _stream(dev))
+    stream, ws = _stream_and_workspace(dev, ws)
+    if dz is None:
+        dz = _empty_rows(rows, vocab, dz_dtype or z.dtype, dev)
+        ld_dz = dz.stride(0)
+    st = lib.opd_topk_loss_bwd(*args, row_stats.data_ptr(), _ptr(grad_loss), dz.data_ptr(), _dtype_code(dz), ld_dz,
+                               ws.data_ptr(), ws.numel(), stream)
     _check("opd_topk_loss_bwd", st)
     return dz
 
 
+@_on_device
 def topk_fused_fwd_bwd(z, top_index, top_logit, rest_lse, alpha: float, tau: float, kl: str = "reverse",
                        grad_loss=None, dz_dtype=None, scratch=None, out=None, ws=None) -> dict:
     """topk_loss_fwd and topk_loss_bwd in one call (opd_topk_fused_fwd_bwd). Returns a dict of loss [R] f32,
@@ -973,21 +1001,21 @@ def topk_fused_fwd_bwd(z, top_index, top_logit, rest_lse, alpha: float, tau: flo
         _require(o.get("row_stats") is not None, "out['row_stats'] is missing")
         _rows_matrix(o["row_stats"], "row_stats", rows, 4, torch.float32)
         _require(o.get("dz") is not None, "out['dz'] is missing")
-        _dz_arg(o["dz"], z, rows, vocab)
+        ld_dz = _dz_arg(o["dz"], z, rows, vocab)
     dev = z.device
     _same_device(dev, lists + [("grad_loss", grad_loss), ("scratch", scratch)]
                  + [(n, o.get(n)) for n in ("loss", "row_stats", "dz")])
     lib = load_library()
-    with _device_guard(dev):
-        ws = _workspace_arg(ws, dev)
-        scratch = _scratch_arg(scratch, lib.opd_topk_loss_scratch_size(rows, vocab, args[1]), dev)
-        if not o:
-            o["loss"] = torch.empty(rows, dtype=torch.float32, device=dev)
-            o["row_stats"] = torch.empty(rows, 4, dtype=torch.float32, device=dev)
-            o["dz"] = _empty_rows(rows, vocab, dz_dtype or z.dtype, dev)
-        dzp, _, _, ld_dz = _matrix(o["dz"], "dz", whole_vectors=False)
-        st = lib.opd_topk_fused_fwd_bwd(*args, _ptr(grad_loss), o["loss"].data_ptr(), o["row_stats"].data_ptr(), dzp,
-                                        _dtype_code(o["dz"]), ld_dz, _ptr(scratch), _nbytes(scratch), ws.data_ptr(),
-                                        ws.numel(), _stream(dev))
+    stream, ws = _stream_and_workspace(dev, ws)
+    scratch = _scratch_arg(scratch, lib.opd_topk_loss_scratch_size(rows, vocab, args[1]), dev)
+    if not o:
+        o["loss"] = torch.empty(rows, dtype=torch.float32, device=dev)
+        o["row_stats"] = torch.empty(rows, 4, dtype=torch.float32, device=dev)
+        o["dz"] = _empty_rows(rows, vocab, dz_dtype or z.dtype, dev)
+        ld_dz = o["dz"].stride(0)
+    dz = o["dz"]
+    st = lib.opd_topk_fused_fwd_bwd(*args, _ptr(grad_loss), o["loss"].data_ptr(), o["row_stats"].data_ptr(),
+                                    dz.data_ptr(), _dtype_code(dz), ld_dz, _ptr(scratch), _nbytes(scratch),
+                                    ws.data_ptr(), ws.numel(), stream)
     _check("opd_topk_fused_fwd_bwd", st)
     return o
