@@ -7,10 +7,10 @@
 // one read and one write of every logit, so HBM bounds it: the token counts must not cost a pass of
 // their own. A workgroup takes a tile of one block's vocabulary and all of the block's rows (or
 // every gridDim.z-th group of kRowGroup rows): it scans the request's history once, counting the
-// tile's tokens in LDS, turns the counts into one fp32 number to subtract and two bits per token
-// (known; counted in the output), and streams its rows past that state, several vectors in flight per
-// thread. The proposals of a block's earlier rows are added on the way, by the thread that holds the
-// token. (A history of H tokens is read by every tile, from the L2: 4 H bytes a tile against 32 KB a row.)
+// tile's tokens in LDS, and streams its rows past the counts, which a thread turns into factors and a
+// number to subtract once per vector, several vectors in flight per thread. The proposals of a block's
+// earlier rows are added on the way, by the thread that holds the token. (A history of H tokens is read by
+// every tile, from the L2: 4 H bytes a tile against 32 KB a row.)
 
 #include <stdint.h>
 
@@ -32,7 +32,7 @@ __device__ __forceinline__ int clamp_len(const int32_t* p, int b, int most, bool
 
 // Whether a block's rows have a mask that allows nothing, or a number that is none.
 __device__ void check_masks(const AdjustParams& P, int start, int nb) {
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, T = blockDim.x;
   for (int j0 = blockIdx.z * kRowGroup; j0 < nb; j0 += gridDim.z * kRowGroup)
     for (int j = j0; j < min(j0 + kRowGroup, nb); ++j) {
       const int mr = P.mask_row ? P.mask_row[start + j] : start + j;
@@ -44,7 +44,7 @@ __device__ void check_masks(const AdjustParams& P, int start, int nb) {
       const uint32_t* m = reinterpret_cast<const uint32_t*>(P.mask + (int64_t)mr * P.ld_mask_bytes);
       const int words = (P.vocab + 31) / 32;
       bool any = false;
-      for (int w0 = 0; w0 < words && !any; w0 += kThreads) {
+      for (int w0 = 0; w0 < words && !any; w0 += T) {
         const int w = w0 + tid;
         uint32_t bits = w < words ? m[w] : 0u;
         if (w == words - 1 && (P.vocab & 31)) bits &= (1u << (P.vocab & 31)) - 1u;
@@ -54,14 +54,18 @@ __device__ void check_masks(const AdjustParams& P, int start, int nb) {
     }
 }
 
-// STATE: with penalties or biases (else masks alone, and no LDS).
-template <bool BF16, bool STATE>
-__global__ void __launch_bounds__(kThreads) k_adjust(AdjustParams P) {
+// What the rows need of the token state: nothing (masks alone), counts, counts and biases.
+enum State : int { kNone = 0, kCounts = 1, kBiases = 2 };
+
+template <bool BF16, int STATE, int T>
+__global__ void __launch_bounds__(T) k_adjust(AdjustParams P) {
   using V = Vec<BF16>;
   constexpr int EPV = V::EPV;
-  constexpr int kTok = STATE ? kTileVec * EPV : 64;
-  __shared__ float sub[kTok];  // first a bias entry's number, then the token's count, then what to subtract
-  __shared__ uint64_t known[kTok / 64], counted[kTok / 64];
+  constexpr int kTok = kTileVec * EPV;
+  __shared__ __attribute__((aligned(16))) uint32_t count[STATE >= kCounts ? kTok : 4];
+  __shared__ __attribute__((aligned(16))) uint32_t prompt[STATE >= kCounts ? kTok / 32 : 4];  // token in the prompt
+  // a bias entry's number (from 1), then, as fp32, the bias of the entry that counts
+  __shared__ __attribute__((aligned(16))) uint32_t bias[STATE >= kBiases ? kTok : 4];
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
   const int start = P.offsets[b], end = P.offsets[b + 1];
   if (start < 0 || end < start || end > P.n_rows) {
@@ -72,6 +76,7 @@ __global__ void __launch_bounds__(kThreads) k_adjust(AdjustParams P) {
   if ((int)blockIdx.x == P.tiles) return check_masks(P, start, nb);  // the workgroups behind the tiles
   const int v0 = blockIdx.x * P.tile_vec;
   const int nv = min(P.tile_vec, P.nvec - v0);  // vectors of the tile
+  const int n_u = (nv + T - 1) / T;
   const int t0 = v0 * EPV;
   const unsigned nt = (unsigned)(min((v0 + nv) * EPV, P.vocab) - t0);  // tokens of the tile
 
@@ -87,105 +92,33 @@ __global__ void __launch_bounds__(kThreads) k_adjust(AdjustParams P) {
   const int32_t* hist = P.history + (int64_t)b * P.ld_history;
   const int32_t* btok = P.bias_tokens + (int64_t)b * P.ld_bias;
   const float* bval = P.bias_values + (int64_t)b * P.ld_bias;
-  uint32_t* count = reinterpret_cast<uint32_t*>(sub);
 
   for (int j0 = blockIdx.z * kRowGroup; j0 < nb; j0 += gridDim.z * kRowGroup) {
     const int rows = min(kRowGroup, nb - j0);
-    if constexpr (STATE) {
-      __syncthreads();  // the previous group's rows are done with the state
-      for (int i = tid; i < nv * EPV; i += kThreads) count[i] = 0u;
-      for (int i = tid; i < kTok / 64; i += kThreads) known[i] = 0u;
-      __syncthreads();
-      // Which bias entries count: the last of a token's, found as the largest number in its slot.
-      uint64_t mine = 0;  // entries tid, tid + kThreads, ... of this thread that count
-      if (n_bias) {
-        for (int i = tid; i < n_bias; i += kThreads) {
-          const unsigned t = (unsigned)(btok[i] - t0);
-          if ((unsigned)btok[i] >= (unsigned)P.vocab) bad_token = true;
-          else if (t < nt) atomicMax(&count[t], (uint32_t)i + 1u);
-        }
-        __syncthreads();
-        int q = 0;
-        for (int i = tid; i < n_bias; i += kThreads, ++q) {
-          const unsigned t = (unsigned)(btok[i] - t0);
-          if ((unsigned)btok[i] < (unsigned)P.vocab && t < nt && count[t] == (uint32_t)i + 1u) mine |= 1ull << q;
-        }
-        __syncthreads();
-        q = 0;
-        for (int i = tid; i < n_bias; i += kThreads, ++q)
-          if (mine >> q & 1) count[btok[i] - t0] = 0u;
-        __syncthreads();
-      }
-      // Counts: the history, then the proposals of the block's rows before this group.
-      auto see = [&](int tok, bool prompt) {
-        bad_token |= (unsigned)tok >= (unsigned)P.vocab;
-        const unsigned t = (unsigned)(tok - t0);
-        if (t < nt && (unsigned)tok < (unsigned)P.vocab) {
-          if (prompt)
-            atomicOr(reinterpret_cast<uint32_t*>(known) + (t >> 5), 1u << (t & 31));
-          else
-            atomicAdd(&count[t], 1u);
-        }
-      };
-      constexpr int Q = 16;  // tokens in flight per thread
-      int i = 0;
-      for (; i + Q * kThreads <= n_hist; i += Q * kThreads) {
-        struct alignas(4) Four { int32_t t[4]; };  // (16 bytes at once, of any row pitch)
-        Four f[Q / 4];
-#pragma unroll
-        for (int q = 0; q < Q / 4; ++q) f[q] = *reinterpret_cast<const Four*>(hist + i + 4 * (q * kThreads + tid));
-#pragma unroll
-        for (int q = 0; q < Q / 4; ++q)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) see(f[q].t[e], i + 4 * (q * kThreads + tid) + e < n_prompt);
-      }
-#pragma unroll 4
-      for (int h = i + tid; h < n_hist; h += kThreads) see(hist[h], h < n_prompt);
-      if (P.draft)
-        for (int h = tid; h < j0; h += kThreads) see(P.draft[start + h], false);
-      __syncthreads();
-      for (int t = tid; t < (nv * EPV + 63) / 64 * 64; t += kThreads) {
-        const uint32_t c = t < nv * EPV ? count[t] : 0u;
-        if (t < nv * EPV) sub[t] = c ? __builtin_fmaf(freq, (float)c, pres) : 0.f;
-        const uint64_t bits = __builtin_amdgcn_ballot_w64(c != 0u);
-        if (lane == 0) {
-          counted[t >> 6] = bits;
-          known[t >> 6] |= bits;
-        }
-      }
-      __syncthreads();
-      if (mine) {
-        int q = 0;
-        for (int k = tid; k < n_bias; k += kThreads, ++q)
-          if (mine >> q & 1) sub[btok[k] - t0] -= bval[k];
-      }
-      __syncthreads();
-    }
-
+    const int items = n_u * rows;
     // Lane j: the proposal before the group's row j, and the row's mask (one that is none: -1).
     const int mine_row = start + j0 + lane;
-    const int lane_tok = STATE && P.draft && lane < rows && j0 + lane > 0 ? P.draft[mine_row - 1] : -1;
+    const int lane_tok = STATE >= kCounts && P.draft && lane < rows && j0 + lane > 0 ? P.draft[mine_row - 1] : -1;
     int lane_mask = -1;
     if (P.mask && lane < rows) lane_mask = P.mask_row ? P.mask_row[mine_row] : mine_row;
     if (lane_mask >= P.n_masks) lane_mask = -1;
 
-    // The tile's vectors, kThreads at a time, and for each the group's rows: items (u, j) in that order,
+    // The tile's vectors, T at a time, and for each the group's rows: items (u, j) in that order,
     // kAhead of them loaded ahead of the one that is worked on.
-    const int n_u = (nv + kThreads - 1) / kThreads, items = n_u * rows;
     u32x4 raw[kAhead];
     uint32_t bits[kAhead];
     int load_u = 0, load_j = 0, u = 0, j = 0;
     auto load = [&](u32x4& to, uint32_t& allowed) {
       const int64_t row = start + j0 + load_j;
       const RowBuf in = row_buf(P.x + row * P.ld_bytes + (int64_t)v0 * 16, (uint32_t)nv * 16u);
-      to = buf_load16<kStream>(in, (uint32_t)tid * 16u, (uint32_t)(load_u * kThreads) * 16u);
+      to = buf_load16<kStream>(in, (uint32_t)tid * 16u, (uint32_t)(load_u * T) * 16u);
       if (P.mask) {
         const int mr = __builtin_amdgcn_readlane(lane_mask, load_j);
         // a bf16 vector has a byte of the mask, an fp32 vector half of one; without a mask nothing is read
         const int64_t first = BF16 ? v0 : v0 >> 1;
         const RowBuf m = row_buf(P.mask + max(mr, 0) * P.ld_mask_bytes + first,
                                  mr < 0 ? 0u : (uint32_t)(BF16 ? nv : (nv + 1) >> 1));
-        const uint32_t at = (uint32_t)(BF16 ? load_u * kThreads : load_u * kThreads / 2);
+        const uint32_t at = (uint32_t)(BF16 ? load_u * T : load_u * T / 2);
         const uint32_t byte = __builtin_amdgcn_raw_buffer_load_b8(m.r, BF16 ? tid : tid >> 1, (int)min(at, m.bytes), 0);
         allowed = BF16 ? byte : byte >> (4 * (tid & 1));
       }
@@ -194,6 +127,73 @@ __global__ void __launch_bounds__(kThreads) k_adjust(AdjustParams P) {
         ++load_u;
       }
     };
+    each<kAhead>([&](auto d) { load(raw[d], bits[d]); });
+
+    if constexpr (STATE >= kCounts) {
+      lds_barrier();  // the previous group's rows are done with the state
+      const u32x4 zero = {0, 0, 0, 0};
+      for (int i = tid; i < n_u * T * EPV / 4; i += T) {
+        reinterpret_cast<u32x4*>(count)[i] = zero;
+        if constexpr (STATE >= kBiases) reinterpret_cast<u32x4*>(bias)[i] = zero;
+      }
+      for (int i = tid; i < kTok / 128; i += T) reinterpret_cast<u32x4*>(prompt)[i] = zero;
+      lds_barrier();
+      if constexpr (STATE >= kBiases)  // the last entry of a token counts: the largest number in its slot
+        for (int i = tid; i < n_bias; i += T) {
+          const int tok = btok[i];
+          bad_token |= (unsigned)tok >= (unsigned)P.vocab;
+          if ((unsigned)tok < (unsigned)P.vocab && (unsigned)(tok - t0) < nt) atomicMax(&bias[tok - t0], (uint32_t)i + 1u);
+        }
+      // the history, then the proposals of the block's rows before this group
+      auto see = [&](int tok, bool in_prompt) {
+        bad_token |= (unsigned)tok >= (unsigned)P.vocab;
+        const unsigned t = (unsigned)(tok - t0);
+        if (t < nt && (unsigned)tok < (unsigned)P.vocab) {
+          if (in_prompt)
+            atomicOr(&prompt[t >> 5], 1u << (t & 31));
+          else
+            atomicAdd(&count[t], 1u);
+        }
+      };
+      constexpr int Q = 4;  // 16-byte loads in flight per thread
+      struct alignas(4) Four { int32_t t[4]; };  // (of any row pitch)
+      int i = 0;
+      for (; i + 4 * Q * T <= n_hist; i += 4 * Q * T) {
+        Four f[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) f[q] = *reinterpret_cast<const Four*>(hist + i + 4 * (q * T + tid));
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) see(f[q].t[e], i + 4 * (q * T + tid) + e < n_prompt);
+      }
+      for (; i < n_hist; i += 4 * T) {
+        int f[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) f[q] = i + q * T + tid < n_hist ? hist[i + q * T + tid] : t0 + (int)nt;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (i + q * T + tid < n_hist) see(f[q], i + q * T + tid < n_prompt);
+      }
+      if (P.draft)
+        for (int h = tid; h < j0; h += T) see(P.draft[start + h], false);
+      lds_barrier();
+      if constexpr (STATE >= kBiases) {
+        uint64_t mine = 0;  // entries tid, tid + T, ... of this thread that count
+        int q = 0;
+        for (int k = tid; k < n_bias; k += T, ++q) {
+          const int tok = btok[k];
+          if ((unsigned)tok < (unsigned)P.vocab && (unsigned)(tok - t0) < nt && bias[tok - t0] == (uint32_t)k + 1u)
+            mine |= 1ull << q;
+        }
+        lds_barrier();
+        q = 0;
+        for (int k = tid; k < n_bias; k += T, ++q)
+          if (mine >> q & 1) bias[btok[k] - t0] = __float_as_uint(bval[k]);
+        lds_barrier();
+      }
+    }
+
     float s[EPV], up[EPV], down[EPV];  // what to subtract; factors of a positive and of another logit
     uint32_t kn = 0, co = 0;
     auto factors = [&]() {
@@ -203,18 +203,23 @@ __global__ void __launch_bounds__(kThreads) k_adjust(AdjustParams P) {
         down[e] = (kn >> e & 1) ? rho : 1.f;
       }
     };
-    each<kAhead>([&](auto d) { load(raw[d], bits[d]); });
     for (int it = 0; it < items; it += kAhead) {
       each<kAhead>([&](auto d) {
         if (it + d < items) {
-          const int e0 = (u * kThreads + tid) * EPV, v = v0 + u * kThreads + tid;
+          const int e0 = (u * T + tid) * EPV, v = v0 + u * T + tid;
           const int64_t row = start + j0 + j;
-          if constexpr (STATE) {
+          if constexpr (STATE >= kCounts) {
             if (j == 0) {
+              kn = prompt[e0 >> 5] >> (e0 & 31);
+              co = 0;
 #pragma unroll
-              for (int e = 0; e < EPV; ++e) s[e] = sub[e0 + e];
-              kn = (uint32_t)(known[e0 >> 6] >> (e0 & 63));
-              co = (uint32_t)(counted[e0 >> 6] >> (e0 & 63));
+              for (int e = 0; e < EPV; ++e) {
+                const uint32_t c = count[e0 + e];
+                s[e] = c ? __builtin_fmaf(freq, (float)c, pres) : 0.f;
+                if constexpr (STATE >= kBiases) s[e] -= __uint_as_float(bias[e0 + e]);
+                co |= (c ? 1u : 0u) << e;
+              }
+              kn |= co;
               factors();
             } else {  // the previous row's proposal is part of the output from here on
               const int tok = __builtin_amdgcn_readlane(lane_tok, j);
@@ -232,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) k_adjust(AdjustParams P) {
           }
           float x[EPV];
           V::unpack(raw[d], x);
-          if constexpr (STATE) {
+          if constexpr (STATE >= kCounts) {
 #pragma unroll
             for (int e = 0; e < EPV; ++e) x[e] = __builtin_fmaf(x[e], x[e] > 0.f ? up[e] : down[e], -s[e]);
           }
@@ -243,9 +248,9 @@ __global__ void __launch_bounds__(kThreads) k_adjust(AdjustParams P) {
           uint8_t* o = P.out + row * P.ld_out_bytes;
           // (whole vectors of the tile; a row's last elements one by one)
           const RowBuf out = row_buf(o + (int64_t)v0 * 16, (uint32_t)min(nv, P.vocab / EPV - v0) * 16u);
-          buf_store16_nt(out, (uint32_t)(u * kThreads + tid) * 16u, V::pack(x));
+          buf_store16_nt(out, (uint32_t)(u * T + tid) * 16u, V::pack(x));
           const int valid = P.vocab - v * EPV;
-          if (u * kThreads + tid < nv && valid < EPV) {
+          if (u * T + tid < nv && valid < EPV) {
 #pragma unroll
             for (int e = 0; e < EPV; ++e)
               if (e < valid) V::put(o, v * EPV + e, x[e]);
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__(kThreads) k_adjust(AdjustParams P) {
   }
   if (blockIdx.x == 0) {  // one tile sees every list whole
     if (P.draft)
-      for (int j = tid; j < nb; j += kThreads) bad_token |= (unsigned)P.draft[start + j] >= (unsigned)P.vocab;
+      for (int j = tid; j < nb; j += T) bad_token |= (unsigned)P.draft[start + j] >= (unsigned)P.vocab;
     if (bad_token) atomicOr(P.flags, kFlagBadToken);
     if (bad_list) atomicOr(P.flags, kFlagBadList);
   }
@@ -273,11 +278,12 @@ hipError_t launch_adjust(const AdjustParams& p, int in_bf16, hipStream_t s) {
   // row groups of a block of average length, one for each layer of the grid
   int64_t z = (p.n_rows + (int64_t)p.n_blocks * kRowGroup - 1) / ((int64_t)p.n_blocks * kRowGroup);
   z = z < 1 ? 1 : z > 4096 ? 4096 : z;
+  const int state = p.bias_tokens ? kBiases : p.history || p.draft ? kCounts : kNone;
+  const int threads = state == kNone ? 256 : 512;
   // smaller tiles where the blocks are too few to fill the device
   int tile = kTileVec;
-  while (tile > kThreads && (int64_t)p.n_blocks * z * ((p.nvec + tile - 1) / tile) < 1024) tile /= 2;
+  while (tile > threads && (int64_t)p.n_blocks * z * ((p.nvec + tile - 1) / tile) < 1024) tile /= 2;
   const int tiles = (p.nvec + tile - 1) / tile;
-  const bool state = p.history || p.draft || p.bias_tokens;
   for (int b0 = 0; b0 < p.n_blocks; b0 += 65535) {  // the grid's second dimension ends there
     AdjustParams q = p;
     q.tile_vec = tile;
@@ -294,14 +300,12 @@ hipError_t launch_adjust(const AdjustParams& p, int in_bf16, hipStream_t s) {
     if (q.bias_values) q.bias_values += (int64_t)b0 * p.ld_bias;
     if (q.bias_len) q.bias_len += b0;
     const dim3 grid((unsigned)(tiles + (p.mask ? 1 : 0)), (unsigned)q.n_blocks, (unsigned)z);
-    if (in_bf16 && state)
-      hipLaunchKernelGGL((k_adjust<true, true>), grid, dim3(kThreads), 0, s, q);
-    else if (in_bf16)
-      hipLaunchKernelGGL((k_adjust<true, false>), grid, dim3(kThreads), 0, s, q);
-    else if (state)
-      hipLaunchKernelGGL((k_adjust<false, true>), grid, dim3(kThreads), 0, s, q);
+    if (state == kBiases)
+      hipLaunchKernelGGL((in_bf16 ? k_adjust<true, kBiases, 512> : k_adjust<false, kBiases, 512>), grid, dim3(512), 0, s, q);
+    else if (state == kCounts)
+      hipLaunchKernelGGL((in_bf16 ? k_adjust<true, kCounts, 512> : k_adjust<false, kCounts, 512>), grid, dim3(512), 0, s, q);
     else
-      hipLaunchKernelGGL((k_adjust<false, false>), grid, dim3(kThreads), 0, s, q);
+      hipLaunchKernelGGL((in_bf16 ? k_adjust<true, kNone, 256> : k_adjust<false, kNone, 256>), grid, dim3(256), 0, s, q);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
