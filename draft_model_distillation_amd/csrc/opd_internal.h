@@ -178,7 +178,7 @@ struct AdjustParams {
 
 // A row's k largest logits and the log-sum-exp of the others (opd_topk.hip).
 constexpr int kTopkMax = OPD_TOPK_MAX;
-constexpr int kTopkCap = 4096;  // candidate keys a workgroup holds in LDS
+constexpr int kTopkCap = 2048;  // candidate keys a workgroup holds in LDS
 struct TopkParams {
   const uint8_t* y;
   int64_t ld_bytes;

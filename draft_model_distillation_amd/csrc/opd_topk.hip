@@ -2,20 +2,22 @@
 //
 // A workgroup takes a segment of a row (the whole row where there are rows enough to fill the device).
 // Its first vectors are loaded into registers at once; the k-th largest of the maxima of groups of
-// threads over them is a lower bound of the k-th largest logit. From there on an element at or above the
-// bound is a candidate and goes, as a 64-bit key (value's order in the upper half, falling index in the
-// lower, so that no two are the same), into a buffer in LDS, and any other adds 2^((x - bound) log2 e) to
-// its thread's sum; what is not in registers is streamed past the same bound. Candidates are few (for
-// random order k times the segment's length over the held part's). They are ranked by counting, the k
-// largest are the answer, and the others join the sums in the order of their rank. The sum of the others
-// is never formed by subtracting the listed ones, which would lose what is left where the list holds
-// nearly all of the row; where the bound turns out to be no reference for it (all others so far below
-// that their terms vanish), the segment is gone over once more for the sum alone.
+// threads over them is a lower bound of the k-th largest logit. From there on a vector with an element at
+// or above the bound is put on a list, and any other adds its 2^((x - bound) log2 e) to its thread's sum;
+// what is not in registers is streamed past the same bound. Listed vectors are few; as many threads take
+// them from LDS, their elements at or above the bound being the candidates: 64-bit keys (value's order in
+// the upper half, falling index in the lower, so that no two are the same) in a buffer in LDS. A search
+// over the keys' bits separates the k largest, which are ordered and are the answer. The sum of the others
+// is never formed by subtracting the listed ones, which would lose what is left where the list holds nearly
+// all of the row; where the bound turns out to be no reference for it (all others so far below that their
+// terms vanish), the segment is gone over once more for the sum alone.
 //
-// When the buffer would run over (rows of equal values; rising rows), it is cut to the k largest and the
-// bound raised to the k-th, after every few vectors if need be. Every set and every order of additions
-// depends on the data alone, not on the order in which candidates reach the buffer, so results are the
-// same bits every time.
+// When list or buffer would run over (rows of equal values; rising rows), the vectors in question are gone
+// over in order, the buffer is cut to the k largest and the bound raised to the k-th as often as needed.
+//
+// Results are the same bits every time: every set depends on the data alone, sums are taken in a fixed
+// order, and the terms of listed vectors and of candidates that are left over, which come in any order,
+// are added as whole multiples of 2^-45 of their reference.
 //
 // This file is compiled with the IEEE mode off, like the row kernels: NaN is outside the contract.
 
@@ -30,8 +32,14 @@ namespace opd {
 namespace {
 
 constexpr int kLoose = 4;        // vectors in flight per thread of what is not held
-constexpr int kBatch = 256;      // threads that append between two checks where the buffer runs over
-constexpr int kRankMost = 512;   // candidates up to which ranking by counting beats sorting
+constexpr int kGroup = 4;        // times those between two looks at the list
+constexpr int kBatch = 128;      // threads that append between two checks where the buffer runs over
+constexpr int kListMost = 1024;  // vectors with candidates between two looks at them
+constexpr int kSearchMost = 1024;  // candidates up to which one wave's search beats sorting all of them
+constexpr int kSortedMost = 512;
+constexpr int kRankMost = 128;   // keys up to which ranking by counting beats sorting
+constexpr float kUnit = 0x1p45f; // one over the unit of the sums that are taken in any order
+constexpr float kLeastSum = 0x1p-16f;  // least sum, relative to its reference, that these units are fine enough for
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
 
 // Unsigned keys in the order of the values (-0 as +0, so that equal values go by index).
@@ -65,13 +73,16 @@ struct Rest {
 // comes later is higher than theirs.
 __device__ __forceinline__ float bound_after_cut(float kth) { return key_value(order_key(kth) + 1u); }
 
-// The sum of a thread's elements that were no candidates, relative to the bound (none is above it).
+// The sum of a thread's elements that were no candidates, relative to the bound (none is above it): of
+// vectors in the order they came, and in units, of listed ones.
 struct Low {
   float ref, sum = 0.f;
+  uint64_t units = 0;
+  __device__ __forceinline__ float term(float x) const { return ex2(__builtin_fmaf(x, kLog2e, -ref)); }
   __device__ __forceinline__ void rebase(float bound) {
-    const float r = fmaxf(bound * kLog2e, kNoRef);
-    sum *= ex2(ref - r);
-    ref = r;
+    ref = fmaxf(bound * kLog2e, kNoRef);
+    sum = 0.f;
+    units = 0;
   }
 };
 
@@ -81,12 +92,88 @@ __device__ __forceinline__ void settle(u32x4& v, Low& low) { asm volatile("" : "
 
 struct Shared {
   uint64_t keys[kTopkCap];
-  uint64_t sorted[kRankMost];
+  uint64_t sorted[kSortedMost];
+  u32x4 listed_raw[kListMost];
+  uint32_t list[kListMost];
   uint32_t maxima[512];
+  uint64_t units[16][2];
   float pair[16][2];
   float bound;
-  int count;
+  uint32_t least;  // the search's result
+  int count, listed, n_sorted;
+  int again;  // the sum has to be formed anew
 };
+
+// Sum of whole numbers over the wave, in every lane.
+__device__ __forceinline__ uint64_t wave_sum_units(uint64_t x) {
+  auto other = [&](auto lanes) { return ((uint64_t)lanes((uint32_t)(x >> 32)) << 32) | lanes((uint32_t)x); };
+  x += other([](uint32_t v) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true); });
+  x += other([](uint32_t v) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true); });
+  x += other([](uint32_t v) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true); });
+  x += other([](uint32_t v) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true); });
+  const auto lo = __builtin_amdgcn_permlane32_swap((uint32_t)x, (uint32_t)x, false, false);
+  const auto hi = __builtin_amdgcn_permlane32_swap((uint32_t)(x >> 32), (uint32_t)(x >> 32), false, false);
+  x = (((uint64_t)hi[0] << 32) | lo[0]) + (((uint64_t)hi[1] << 32) | lo[1]);
+  const auto l2 = __builtin_amdgcn_permlane16_swap((uint32_t)x, (uint32_t)x, false, false);
+  const auto h2 = __builtin_amdgcn_permlane16_swap((uint32_t)(x >> 32), (uint32_t)(x >> 32), false, false);
+  return (((uint64_t)h2[0] << 32) | l2[0]) + (((uint64_t)h2[1] << 32) | l2[1]);
+}
+
+// A thread's candidates that a cut has left over, in units of 2^ref.
+struct Left {
+  uint64_t units = 0;
+  float ref = kNoRef;
+};
+
+// Adds what the threads hold to thread 0's `rest`. A sum that is too small for its units, if it is the last
+// one (`last`) or of candidates, has to be formed anew: S.again. All threads.
+template <int T>
+__device__ void flush(Shared& S, const Low& low, const Left& left, bool last, Rest& rest) {
+  const int tid = thread_x();
+  uint64_t lu = wave_sum_units(left.units), units = wave_sum_units(low.units);
+  float sum = wave_sum(low.sum);
+  if ((tid & 63) == 0) {
+    S.units[tid >> 6][0] = units;
+    S.units[tid >> 6][1] = lu;
+    S.pair[tid >> 6][0] = sum;
+  }
+  lds_barrier();
+  if (tid < 64) {  // (the waves' float sums in the same tree as the lanes')
+    const bool wave = tid < T / 64;
+    units = wave_sum_units(wave ? S.units[tid][0] : 0);
+    lu = wave_sum_units(wave ? S.units[tid][1] : 0);
+    sum = wave_sum(wave ? S.pair[tid][0] : 0.f);
+    if (tid == 0) {
+      const float all = sum + (float)units * (1.f / kUnit), over = (float)lu * (1.f / kUnit);
+      if ((last && !(all >= kLeastSum)) || (left.ref > kNoRef && over < kLeastSum)) S.again = 1;
+      lse_join(rest.ref, rest.sum, low.ref, all);
+      lse_join(rest.ref, rest.sum, left.ref, over);
+    }
+  }
+  lds_barrier();
+}
+
+// Sorts n keys, the largest first; room for the next power of two from `least` on. All threads.
+template <int T>
+__device__ void sort_keys(uint64_t* keys, int n, int least) {
+  const int tid = thread_x();
+  int m = least;
+  while (m < n) m <<= 1;
+  for (int i = n + tid; i < m; i += T) keys[i] = 0;
+  lds_barrier();
+  for (int size = 2; size <= m; size <<= 1)
+    for (int stride = size >> 1; stride > 0; stride >>= 1) {
+      for (int i = tid; i < m / 2; i += T) {
+        const int a = 2 * i - (i & (stride - 1)), b = a + stride;
+        const uint64_t x = keys[a], y = keys[b];
+        if ((x < y) == ((a & size) == 0)) {
+          keys[a] = y;
+          keys[b] = x;
+        }
+      }
+      lds_barrier();
+    }
+}
 
 // The first bound: the k-th largest of m maxima' keys in S.maxima (one wave; m a multiple of 64), as far as
 // its upper `bits` bits say, rounded down; -inf where there are not k.
@@ -107,41 +194,102 @@ __device__ void find_bound(Shared& S, int k, int bits) {
   if (lane == 0) S.bound = key_value(max(p, kKeyNegInf));
 }
 
-// Orders the n keys in S.keys (largest first), keeps the k largest there and adds the others to the
-// threads' sums in the order of their rank. Returns the number kept; S.bound is the k-th's value. All T
-// threads call it.
+// The largest 32-bit number that at least k of the n > k keys' upper halves reach, or a smaller one that
+// exactly k reach. One wave; R: keys per lane.
+template <int R>
+__device__ void search_keys(Shared& S, int n, int k) {
+  const int lane = thread_x() & 63;
+  uint32_t key[R];
+  uint32_t top = 0, bottom = ~0u;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const bool there = i * 64 + lane < n;
+    key[i] = there ? (uint32_t)(S.keys[i * 64 + lane] >> 32) : 0u;
+    top = max(top, key[i]);
+    bottom = there ? min(bottom, key[i]) : bottom;
+  }
+  top = wave_reduce(top, [](uint32_t a, uint32_t b) { return max(a, b); });
+  bottom = wave_reduce(bottom, [](uint32_t a, uint32_t b) { return min(a, b); });
+  // the bits that all have in common need no search
+  int b = top == bottom ? -1 : 31 - __builtin_clz(top ^ bottom);
+  uint32_t p = b < 0 ? top : b == 31 ? 0u : top >> (b + 1) << (b + 1);
+  for (; b >= 0; --b) {
+    const uint32_t q = p | (1u << b);
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[i] >= q));
+    if (c >= k) p = q;
+    if (c == k) break;
+  }
+  if (lane == 0) {
+    S.least = p;
+    S.n_sorted = 0;
+  }
+}
+
+// Cuts the n keys in S.keys to the k largest, in order; those left over go to `left`, or to `rest` in the
+// order of their rank. Returns the number kept; S.bound is the k-th's value. All T threads call it.
 template <int T>
-__device__ int cut(Shared& S, int n, int k, Rest& rest) {
+__device__ int cut(Shared& S, int n, int k, Left& left, Rest& rest) {
   const int tid = thread_x();
   const uint64_t* from = S.keys;
-  if (n <= kRankMost) {
-    for (int i = tid; i < n; i += T) {
-      const uint64_t mine = S.keys[i];
-      int rank = 0;
-      for (int j = 0; j < n; ++j) rank += S.keys[j] > mine ? 1 : 0;
-      S.sorted[rank] = mine;
+  int m = n;  // keys that are put in order
+  bool searched = false;
+  left = Left{};
+  auto leave = [&](uint64_t key) {
+    left.units += (uint64_t)(ex2(__builtin_fmaf(key_value((uint32_t)(key >> 32)), kLog2e, -left.ref)) * kUnit);
+  };
+  if (n > k && n <= kSearchMost) {
+    if (tid < 64) {
+      if (n <= 256)
+        search_keys<4>(S, n, k);
+      else
+        search_keys<kSearchMost / 64>(S, n, k);
     }
+    lds_barrier();
+    const uint32_t least = S.least;
+    left.ref = fmaxf(key_value(max(least, kKeyNegInf)) * kLog2e, kNoRef);
+    for (int i = tid; i < n; i += T) {
+      const uint64_t key = S.keys[i];
+      if ((uint32_t)(key >> 32) >= least) {
+        const int at = atomicAdd(&S.n_sorted, 1);
+        if (at < kSortedMost) S.sorted[at] = key;
+      } else {
+        leave(key);
+      }
+    }
+    lds_barrier();
+    m = S.n_sorted;
+    searched = m <= kSortedMost;
+    if (searched) {
+      from = S.sorted;
+    } else {  // many equal values: all of them in order after all
+      m = n;
+      left = Left{};
+    }
+  }
+  if (m <= kRankMost) {
+    uint64_t mine = 0;
+    int rank = 0;
+    if (tid < m) {
+      mine = from[tid];
+#pragma unroll 8
+      for (int j = 0; j < m; ++j) rank += from[j] > mine ? 1 : 0;
+    }
+    static_assert(kRankMost <= 256, "one thread per key");
+    lds_barrier();
+    if (tid < m) S.sorted[rank] = mine;
     lds_barrier();
     from = S.sorted;
   } else {
-    int m = 1024;
-    while (m < n) m <<= 1;
-    for (int i = n + tid; i < m; i += T) S.keys[i] = 0;
-    lds_barrier();
-    for (int size = 2; size <= m; size <<= 1)
-      for (int stride = size >> 1; stride > 0; stride >>= 1) {
-        for (int i = tid; i < m / 2; i += T) {
-          const int a = 2 * i - (i & (stride - 1)), b = a + stride;
-          const uint64_t x = S.keys[a], y = S.keys[b];
-          if ((x < y) == ((a & size) == 0)) {
-            S.keys[a] = y;
-            S.keys[b] = x;
-          }
-        }
-        lds_barrier();
-      }
+    sort_keys<T>(const_cast<uint64_t*>(from), m, 256);
   }
-  for (int i = k + tid; i < n; i += T) rest.add(key_value((uint32_t)(from[i] >> 32)));
+  for (int i = k + tid; i < m; i += T) {
+    if (searched)
+      leave(from[i]);
+    else
+      rest.add(key_value((uint32_t)(from[i] >> 32)));
+  }
   const int kept = min(n, k);
   if (from != S.keys)
     for (int i = tid; i < kept; i += T) S.keys[i] = from[i];
@@ -184,57 +332,47 @@ __device__ void write_row(const TopkParams& P, const Shared& S, int row, int kep
                           : kNegInf;
 }
 
-// One vector: candidates into the buffer, the others into the sum. The few lanes with candidates are taken
-// one by one, the wave's first lanes trying one element each.
-template <bool BF16>
-__device__ __forceinline__ void take(Shared& S, float bound, Low& low, const u32x4& raw, float (&x)[Vec<BF16>::EPV],
-                                     int first, int end) {
-  using V = Vec<BF16>;
-  constexpr int EPV = V::EPV;
+// One vector: onto the list, or into the sum.
+template <int EPV>
+__device__ __forceinline__ void take(Shared& S, float bound, Low& low, const u32x4& raw, const float (&x)[EPV], int v) {
   float m = x[0];
 #pragma unroll
   for (int e = 1; e < EPV; ++e) m = fmaxf(m, x[e]);
-  uint64_t lanes = __builtin_amdgcn_ballot_w64(m >= bound);
-  if (lanes) {
-    const int lane = thread_x() & 63;
-    do {
-      const int from = __builtin_ctzll(lanes);
-      lanes &= lanes - 1;
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = (uint32_t)__builtin_amdgcn_readlane((int)raw[j], from);
-      const int at = __builtin_amdgcn_readlane(first, from) + lane;
-      const int j = BF16 ? lane >> 1 : lane;
-      const uint32_t word = j == 0 ? w[0] : j == 1 ? w[1] : j == 2 ? w[2] : w[3];
-      const float v = __uint_as_float(!BF16 || (lane & 1) ? word & (BF16 ? 0xffff0000u : ~0u) : word << 16);
-      if (lane < EPV && v >= bound && at < end) {
-        const int place = atomicAdd(&S.count, 1);
-        if (place < kTopkCap) S.keys[place] = make_key(v, at);
+  const bool cand = m >= bound;
+  if (__builtin_amdgcn_ballot_w64(cand)) {
+    if (cand) {
+      const int at = atomicAdd(&S.listed, 1);
+      if (at < kListMost) {
+        S.list[at] = (uint32_t)v;
+        S.listed_raw[at] = raw;
       }
-    } while (lanes);
-#pragma unroll
-    for (int e = 0; e < EPV; ++e) x[e] = x[e] >= bound ? kNegInf : x[e];
+    }
   }
   float s = 0.f;
 #pragma unroll
-  for (int e = 0; e < EPV; ++e) s += ex2(__builtin_fmaf(x[e], kLog2e, -low.ref));
-  low.sum += s;
+  for (int e = 0; e < EPV; ++e) s += low.term(x[e]);
+  low.sum += cand ? 0.f : s;
 }
 
-// The candidates of one vector per thread again, in batches of threads, cutting the buffer before it could
-// run over (`was`: the bound that take() went by; the others are in the sum already). All threads.
+// The vectors that take() listed, one per thread, once more: elements go into the buffer or to thread `rest`,
+// in batches of threads, the buffer being cut before it could run over. All threads.
 template <int EPV, int T>
-__device__ void take_again(Shared& S, float& bound, float was, Rest& rest, const float (&x)[EPV], int first, int end,
-                           int& n, int k) {
+__device__ void take_again(Shared& S, float& bound, float was, const Low& none, Rest& rest, const float (&x)[EPV],
+                           int first, int end, int& n, int k) {
+  float m = x[0];
+#pragma unroll
+  for (int e = 1; e < EPV; ++e) m = fmaxf(m, x[e]);
   for (int b = 0; b < T / kBatch; ++b) {
     if (n + kBatch * EPV > kTopkCap) {
-      n = cut<T>(S, n, k, rest);
+      Left left;
+      n = cut<T>(S, n, k, left, rest);
       if (n == k) bound = bound_after_cut(S.bound);
+      flush<T>(S, none, left, false, rest);
     }
-    if (thread_x() / kBatch == b) {
+    if (thread_x() / kBatch == b && m >= was) {
 #pragma unroll
       for (int e = 0; e < EPV; ++e)
-        if (x[e] >= was && first + e < end) {
+        if (first + e < end) {
           if (x[e] >= bound)
             S.keys[atomicAdd(&S.count, 1)] = make_key(x[e], first + e);
           else
@@ -260,7 +398,7 @@ __global__ void __launch_bounds__(T) k_topk(TopkParams P) {
   const int v0 = seg * P.seg_vec, n_vec = min(P.seg_vec, P.nvec - v0), k = P.k;
   const int base = v0 * EPV, end = min((v0 + n_vec) * EPV, P.vocab);  // tokens [base, end)
   const RowBuf in = row_buf(P.y + (int64_t)row * P.ld_bytes + (int64_t)v0 * 16, (uint32_t)n_vec * 16u);
-  if (tid == 0) S.count = 0;
+  if (tid == 0) S.count = S.listed = S.again = 0;
 
   // Vector v + tid; its elements past the segment's end become -inf.
   auto unpack = [&](u32x4& raw, int v, float (&x)[EPV]) {
@@ -272,11 +410,9 @@ __global__ void __launch_bounds__(T) k_topk(TopkParams P) {
   };
 
   u32x4 held[H];
-#pragma unroll
-  for (int i = 0; i < H; ++i) held[i] = buf_load16<kStream>(in, (uint32_t)tid * 16u, (uint32_t)(i * T) * 16u);
+  each<H>([&](auto i) { held[i] = buf_load16<kStream>(in, (uint32_t)tid * 16u, (uint32_t)(i * T) * 16u); });
   float m = kNegInf;
-#pragma unroll
-  for (int i = 0; i < H; ++i)
+  each<H>([&](auto i) {
     if (i * T < n_vec) {
       if (base + (i * T + T) * EPV > end) {
         float x[EPV];
@@ -288,6 +424,7 @@ __global__ void __launch_bounds__(T) k_topk(TopkParams P) {
       }
       asm volatile("" : "+v"(held[i]), "+v"(m));
     }
+  });
   {
     constexpr int G = T / M;  // threads per maximum: neighbours
     static_assert(G == 1 || G == 2 || G == 4, "maxima of one, two or four lanes");
@@ -304,81 +441,100 @@ __global__ void __launch_bounds__(T) k_topk(TopkParams P) {
   Rest rest;
   Low low;
   low.ref = fmaxf(bound * kLog2e, kNoRef);
-#pragma unroll
-  for (int i = 0; i < H; ++i)
+  each<H>([&](auto i) {
     if (i * T < n_vec) {
       float x[EPV];
       unpack(held[i], i * T, x);
-      take<BF16>(S, bound, low, held[i], x, base + (i * T + tid) * EPV, end);
+      take<EPV>(S, bound, low, held[i], x, i * T + tid);
       settle(held[i], low);
     }
-  // What has been gone over ends at vector g1: the held ones, then U per thread at a time.
+  });
+  // Vectors [g0, g1) are gone over between two looks at the list: the held ones, then kGroup * U per thread.
   int n = 0, g0 = 0, g1 = H * T;
   for (;;) {
-    if (g0 > 0) {
-      u32x4 raw[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) raw[u] = buf_load16<kStream>(in, (uint32_t)tid * 16u, (uint32_t)(g0 + u * T) * 16u);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float x[EPV];
-        unpack(raw[u], g0 + u * T, x);
-        take<BF16>(S, bound, low, raw[u], x, base + (g0 + u * T + tid) * EPV, end);
-        settle(raw[u], low);
+    if (g0 > 0)
+      for (int v = g0; v < g1 && v < n_vec; v += U * T) {
+        u32x4 raw[U];
+        each<U>([&](auto u) { raw[u] = buf_load16<kStream>(in, (uint32_t)tid * 16u, (uint32_t)(v + u * T) * 16u); });
+        each<U>([&](auto u) {
+          float x[EPV];
+          unpack(raw[u], v + u * T, x);
+          take<EPV>(S, bound, low, raw[u], x, v + u * T + tid);
+          settle(raw[u], low);
+        });
       }
-    }
     const bool last = g1 >= n_vec;
     lds_barrier();
-    const int total = S.count;
-    lds_barrier();
-    if (total <= kTopkCap) {
-      n = total;
-    } else {
-      // more candidates than places: back to the keys of before, and those vectors again
-      if (tid == 0) S.count = n;
+    const int listed = S.listed;
+    int total = n;
+    Low more = low;  // with the listed vectors' elements
+    if (listed <= kListMost) {
+      for (int i = tid; i < listed; i += T) {
+        const int v = (int)S.list[i];
+        float x[EPV];
+        V::unpack(S.listed_raw[i], x);
+        const int first = base + v * EPV;
+#pragma unroll
+        for (int e = 0; e < EPV; ++e)
+          if (first + e < end) {
+            if (x[e] >= bound) {
+              const int at = atomicAdd(&S.count, 1);
+              if (at < kTopkCap) S.keys[at] = make_key(x[e], first + e);
+            } else {
+              more.units += (uint64_t)(more.term(x[e]) * kUnit);
+            }
+          }
+      }
       lds_barrier();
-      const float was = bound;
+      total = S.count;
+    }
+    lds_barrier();
+    const bool fits = listed <= kListMost && total <= kTopkCap;
+    if (tid == 0) {
+      S.listed = 0;
+      if (!fits) S.count = n;
+    }
+    const float was = bound;
+    if (fits) {
+      n = total;
+      low = more;
+      lds_barrier();
+    } else {
+      // back to the keys of before, and those vectors in order
+      lds_barrier();
       for (int v = g0; v < g1 && v < n_vec; v += T) {
         u32x4 raw = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)v * 16u);
         float x[EPV];
         unpack(raw, v, x);
-        take_again<EPV, T>(S, bound, was, rest, x, base + (v + tid) * EPV, end, n, k);
+        take_again<EPV, T>(S, bound, was, Low{low.ref}, rest, x, base + (v + tid) * EPV, end, n, k);
       }
+    }
+    Left left;
+    if (last || n > kTopkCap / 2) {
+      n = cut<T>(S, n, k, left, rest);
+      if (n == k && !last) bound = bound_after_cut(S.bound);
+    }
+    if (last || bound != was) {  // (a sum to which a higher bound's will be added need not be fine)
+      flush<T>(S, low, left, last, rest);
       low.rebase(bound);
     }
     if (last) break;
-    if (n > kTopkCap / 4) {
-      n = cut<T>(S, n, k, rest);
-      if (n == k) bound = bound_after_cut(S.bound);
-      low.rebase(bound);
-    }
     g0 = g1;
-    g1 += U * T;
+    g1 += kGroup * U * T;
   }
-  const int kept = cut<T>(S, n, k, rest);
-  // The bound was a reference for the sum if the terms add up to something (2^-40 of the bound's own
-  // leaves those below fp32's smallest number 2^86 times less); else the others again, by themselves.
-  {
-    float t = wave_sum(low.sum);
-    if ((tid & 63) == 0) S.pair[tid >> 6][0] = t;
-    lds_barrier();
-    t = 0.f;
-    for (int w = 0; w < T / 64; ++w) t += S.pair[w][0];
-    lds_barrier();
-    if (t >= 0x1p-40f) {
-      lse_join(rest.ref, rest.sum, low.ref, low.sum);
-    } else {
-      rest = Rest{};
-      const uint64_t least = kept == k ? S.keys[k - 1] : 0;
-      for (int v = 0; v < n_vec; v += T) {
-        u32x4 raw = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)v * 16u);
-        float x[EPV];
-        unpack(raw, v, x);
+  const int kept = n;
+  if (S.again) {
+    // The bound was no reference for the sum: the others again, by themselves.
+    rest = Rest{};
+    const uint64_t least = kept == k ? S.keys[k - 1] : 0;
+    for (int v = 0; v < n_vec; v += T) {
+      u32x4 raw = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)v * 16u);
+      float x[EPV];
+      unpack(raw, v, x);
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-          const int i = base + (v + tid) * EPV + e;
-          if (i < end && make_key(x[e], i) < least) rest.add(x[e]);
-        }
+      for (int e = 0; e < EPV; ++e) {
+        const int i = base + (v + tid) * EPV + e;
+        if (i < end && make_key(x[e], i) < least) rest.add(x[e]);
       }
     }
   }
@@ -396,15 +552,15 @@ __global__ void __launch_bounds__(T) k_topk(TopkParams P) {
   }
 }
 
-// One workgroup per row joins the segments' lists and sums: again a bound from the threads' maxima, the keys
-// at or above it ranked, the others added to the sums by the threads that loaded them.
+// One workgroup per row joins the segments' lists and sums: a bound from the threads' maxima, the keys at or
+// above it put in order, the others added to the sums by the threads that loaded them.
 __global__ void __launch_bounds__(kThreads) k_topk_merge(TopkParams P) {
   constexpr int T = kThreads, R = kTopkCap / T;
   __shared__ Shared S;
   const int tid = thread_x(), row = group_x(), k = P.k;
   const int total = P.n_seg * k;
   const uint64_t* keys = P.seg_keys + (int64_t)row * total;
-  uint64_t mine[R];
+  uint64_t mine[R];  // (0: an entry of a list that was not full)
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -423,16 +579,18 @@ __global__ void __launch_bounds__(kThreads) k_topk_merge(TopkParams P) {
   lds_barrier();
   const float bound = S.bound;
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (mine[i] == 0) continue;  // (a list that was not full)
-    const float x = key_value((uint32_t)(mine[i] >> 32));
-    if (x >= bound)
-      S.keys[atomicAdd(&S.count, 1)] = mine[i];
-    else
-      rest.add(x);
-  }
+  for (int i = 0; i < R; ++i)
+    if (mine[i] && key_value((uint32_t)(mine[i] >> 32)) >= bound) S.keys[atomicAdd(&S.count, 1)] = mine[i];
   lds_barrier();
-  const int kept = cut<T>(S, S.count, k, rest);
+  const int n = S.count;
+  lds_barrier();
+  Left left;
+  Rest none;
+  const int kept = cut<T>(S, n, k, left, none);
+  const uint64_t least = kept == k ? S.keys[k - 1] : 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (mine[i] && mine[i] < least) rest.add(key_value((uint32_t)(mine[i] >> 32)));
   join_rest<T>(S, rest);
   write_row<T>(P, S, row, kept, rest);
 }
