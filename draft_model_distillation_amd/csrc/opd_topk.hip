@@ -37,7 +37,6 @@ constexpr int kBatch = 128;      // threads that append between two checks where
 constexpr int kListMost = 1024;  // vectors with candidates between two looks at them
 constexpr int kSearchMost = 1024;  // candidates up to which one wave's search beats sorting all of them
 constexpr int kSortedMost = 512;
-constexpr int kRankMost = 128;   // keys up to which ranking by counting beats sorting
 constexpr float kUnit = 0x1p45f; // one over the unit of the sums that are taken in any order
 constexpr float kLeastSum = 0x1p-16f;  // least sum, relative to its reference, that these units are fine enough for
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
@@ -268,6 +267,7 @@ __device__ int cut(Shared& S, int n, int k, Left& left, Rest& rest) {
       left = Left{};
     }
   }
+  constexpr int kRankMost = T < kSortedMost ? T : kSortedMost;  // one thread per key
   if (m <= kRankMost) {
     uint64_t mine = 0;
     int rank = 0;
@@ -276,7 +276,6 @@ __device__ int cut(Shared& S, int n, int k, Left& left, Rest& rest) {
 #pragma unroll 8
       for (int j = 0; j < m; ++j) rank += from[j] > mine ? 1 : 0;
     }
-    static_assert(kRankMost <= 256, "one thread per key");
     lds_barrier();
     if (tid < m) S.sorted[rank] = mine;
     lds_barrier();
@@ -595,7 +594,21 @@ __global__ void __launch_bounds__(kThreads) k_topk_merge(TopkParams P) {
   write_row<T>(P, S, row, kept, rest);
 }
 
-constexpr int kWholeRows = 192;  // rows from which a workgroup per row is faster than split rows
+// Lists up to this long take the first bound from 256 maxima, longer ones from 512: the bound is the
+// better the fewer maxima it is cut from, but useless when nearly all of them are wanted (50257 fp32 tokens,
+// 2048 rows: k 64 74 against 77 us, k 128 84 against 87, k 256 300 against 100 us).
+constexpr int kFewK = 128;
+// Rows that have a workgroup of 1024 threads each (the CUs' number): alone on a CU the larger workgroup
+// is faster, several smaller ones hide each other's waits (256 rows of 151936 bf16 30 against 35 us, 384
+// rows 51 against 42 us).
+constexpr int kOneEach = 256;
+// A row is split if the rows are few, long, and the lists short: one row of 151936 fp32 logits, k 64, 18
+// split against 26 us whole (32 rows 23 against 28, 64 rows 31 against 28), but 13 us whole against 17
+// with 12565 vectors and 36 against 60 with k 256, since joining the segments costs a launch and their
+// lists. Segments of 2048 vectors, eight a thread: with 1024 16 rows take 22 instead of 20.5 us.
+constexpr int kWholeRows = 48;
+constexpr int kWholeVec = 16384;
+constexpr int kSegVec = 2048;
 
 template <bool BF16, int T, int H, int M>
 hipError_t launch(const TopkParams& p, hipStream_t s) {
@@ -605,23 +618,20 @@ hipError_t launch(const TopkParams& p, hipStream_t s) {
 
 template <bool BF16>
 hipError_t launch_rows(const TopkParams& p, hipStream_t s) {
-  if (p.seg_vec <= 256 * 8) return launch<BF16, 256, 8, 256>(p, s);
-  if (p.seg_vec <= 512 * 10) return launch<BF16, 512, 10, 512>(p, s);
-  if (p.n_rows < 512) return p.k <= 96 ? launch<BF16, 1024, 19, 256>(p, s) : launch<BF16, 1024, 19, 512>(p, s);
-  return p.k <= 96 ? launch<BF16, 512, 12, 256>(p, s) : launch<BF16, 512, 12, 512>(p, s);
+  const bool few = p.k <= kFewK;
+  if (p.seg_vec <= 256 * 8 && few) return launch<BF16, 256, 8, 256>(p, s);
+  if (p.seg_vec > 512 * 10 && p.n_rows <= kOneEach)
+    return few ? launch<BF16, 1024, 19, 256>(p, s) : launch<BF16, 1024, 19, 512>(p, s);
+  return few ? launch<BF16, 512, 10, 256>(p, s) : launch<BF16, 512, 10, 512>(p, s);
 }
 
 }  // namespace
 
 void topk_split(int64_t n_rows, int32_t nvec, int32_t k, int32_t* n_seg, int32_t* seg_vec) {
-  // Few rows: segments for two workgroups of 256 threads per CU, of at least four vectors per thread, and at
-  // most as many as one workgroup can merge.
   int64_t seg = 1;
-  if (n_rows > 0 && n_rows < kWholeRows) {
-    seg = (1024 + n_rows - 1) / n_rows;
-    seg = std::min<int64_t>(seg, (nvec + 4 * kThreads - 1) / (4 * kThreads));
-    seg = std::min<int64_t>(seg, kTopkCap / k);
-    seg = std::max<int64_t>(seg, 1);
+  if (n_rows < kWholeRows && nvec > kWholeVec && k <= kFewK) {
+    seg = (nvec + kSegVec - 1) / kSegVec;
+    seg = std::min<int64_t>(seg, kTopkCap / k);  // what one workgroup can merge
   }
   *seg_vec = (int32_t)(((nvec + seg - 1) / seg + 7) / 8 * 8);
   *n_seg = (nvec + *seg_vec - 1) / *seg_vec;

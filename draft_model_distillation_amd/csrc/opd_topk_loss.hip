@@ -519,7 +519,23 @@ __global__ void __launch_bounds__(kThreads) k_topk_loss_grad(TopkLossParams P) {
   }
 }
 
-constexpr int kHoldRows = 128;  // rows from which a workgroup per row is faster than split rows
+// Rows from which a workgroup per row is faster than segments of rows. Fused (151936 bf16): 96 rows 25 us
+// whole, 18 split, 192 rows 31 and 37. The forward call alone: 128 rows of 151936 fp32 logits 28 us whole,
+// 23.5 split, 192 rows 29 and 31; rows of up to 8192 vectors are faster whole at any number (50257 bf16,
+// 16 rows: 8.5 and 9 to 10 us), as the split call has a second launch.
+constexpr int kHoldRows = 128;
+constexpr int kHoldRowsFwd = 160;
+constexpr int kWholeVecFwd = 8192;
+// Workgroups of segments that few rows are split for: more of them read the lists and join the sums once
+// more (16 rows of 151936 bf16 fused 10.8 us, with 512 workgroups 12.1, with 1024 15.8).
+constexpr int kSplitGroups = 256;
+// The fused call holds a row of up to 4096 vectors in 256 threads (32003 bf16, 2048 rows: 56 us, 61 with
+// 512). Longer ones take 512, two workgroups to a CU whose waits hide each other, though half of a long
+// row is read again (8192 rows of 151936 bf16 996 us, 1050 with 1024); 1024 where each row has a CU to
+// itself (256 rows 37 us, 40 with 512) or what 512 threads do not hold is most of the row (2048 rows of
+// 151936 fp32 487 us, 560 with 512).
+constexpr int kOneEach = 256;
+constexpr int kHoldVec = 28672;
 
 // Launches a kernel with a row's bitmap in LDS (above 64 KiB with the kernel's own for the widest rows,
 // which has to be allowed; the setting is per device, so it is made on every such launch).
@@ -558,8 +574,9 @@ template <bool BF16, bool OUT_BF16>
 hipError_t launch_fused(const TopkLossParams& p, hipStream_t s) {
   if (p.n_rows >= kHoldRows) {
     if (p.nvec <= 256 * 16) return launch_hold<BF16, OUT_BF16, true, 256, 16>(p, s);
-    if (p.nvec <= 512 * 19) return launch_hold<BF16, OUT_BF16, true, 512, 19>(p, s);
-    return launch_hold<BF16, OUT_BF16, true, 1024, 19>(p, s);
+    if (p.nvec > 512 * 19 && (p.n_rows <= kOneEach || p.nvec > kHoldVec))
+      return launch_hold<BF16, OUT_BF16, true, 1024, 19>(p, s);
+    return launch_hold<BF16, OUT_BF16, true, 512, 19>(p, s);
   }
   const hipError_t e = launch_sums<BF16>(p, s);
   return e != hipSuccess ? e : launch_grad<BF16, OUT_BF16, true>(p, s);
@@ -567,7 +584,7 @@ hipError_t launch_fused(const TopkLossParams& p, hipStream_t s) {
 
 template <bool BF16>
 hipError_t launch_fwd(const TopkLossParams& p, hipStream_t s) {
-  if (p.n_rows >= kHoldRows) return launch_hold<BF16, false, false, 512, 0>(p, s);
+  if (p.n_rows >= kHoldRowsFwd || p.nvec <= kWholeVecFwd) return launch_hold<BF16, false, false, 512, 0>(p, s);
   const hipError_t e = launch_sums<BF16>(p, s);
   if (e != hipSuccess) return e;
   return launch_with_bitmap(k_topk_loss_row<BF16>, dim3((unsigned)p.n_rows), 64, p.nvec, Vec<BF16>::EPV, p, s);
@@ -577,7 +594,7 @@ hipError_t launch_fwd(const TopkLossParams& p, hipStream_t s) {
 
 void topk_loss_split(int64_t n_rows, int32_t nvec, int32_t* n_seg, int32_t* seg_vec) {
   // Segments of at most kSegVec vectors; more of them where the rows alone do not fill the device.
-  int64_t seg = n_rows > 0 ? (1024 + n_rows - 1) / n_rows : 1;
+  int64_t seg = n_rows > 0 ? (kSplitGroups + n_rows - 1) / n_rows : 1;
   seg = std::min<int64_t>(seg, (nvec + kThreads - 1) / kThreads);
   seg = std::max<int64_t>(seg, (nvec + kSegVec - 1) / kSegVec);
   *seg_vec = (int32_t)(((nvec + seg - 1) / seg + 7) / 8 * 8);  // (whole bitmap words and 128-byte lines)
@@ -585,7 +602,7 @@ void topk_loss_split(int64_t n_rows, int32_t nvec, int32_t* n_seg, int32_t* seg_
 }
 
 size_t topk_loss_scratch(int64_t n_rows, int32_t nvec) {
-  if (n_rows >= kHoldRows) return 0;
+  if (n_rows >= std::max(kHoldRows, kHoldRowsFwd)) return 0;
   int32_t seg = 1, seg_vec = 0;
   topk_loss_split(n_rows, nvec, &seg, &seg_vec);
   return (size_t)n_rows * seg * 8;
