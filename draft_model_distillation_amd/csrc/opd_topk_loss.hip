@@ -19,8 +19,8 @@
 //   k_topk_loss_hold  one workgroup per row: the row is loaded once and stays in registers between its
 //                     sum and its gradient (what does not fit is read again, from the caches).
 //   k_topk_loss_sums, k_topk_loss_grad, k_topk_loss_row   a row split into segments with a workgroup
-//                     each, for few rows and for the backward call of its own: sums, then (joining
-//                     them) the gradient or, for the forward call, loss and statistics.
+//                     each, for few rows: sums, then (joining them) the gradient or, for the forward
+//                     call, loss and statistics.
 //
 // This file is compiled with the IEEE mode off, like the row kernels: NaN is outside the contract.
 
@@ -293,8 +293,11 @@ __device__ __forceinline__ void grad_vector(const RowBuf& out, int tid, int v, u
   for (int e = 0; e < EPV; ++e) x[e] = factor * ex2(__builtin_fmaf(x[e], kLog2e, -L));
   const uint32_t at = (uint32_t)(tid + v) * kBytes;
   if constexpr (BF16 && !OUT_BF16) {
-    buf_store16_nt(out, at, Vec<false>::pack({x[0], x[1], x[2], x[3]}));
-    buf_store16_nt(out, at + 16, Vec<false>::pack({x[4], x[5], x[6], x[7]}));
+    // (through the caches, which join the halves of a line that a store leaves out: streamed, 1111 rows of
+    // 50257 logits take 114 instead of 74 us)
+    const u32x4 lo = Vec<false>::pack({x[0], x[1], x[2], x[3]}), hi = Vec<false>::pack({x[4], x[5], x[6], x[7]});
+    __builtin_amdgcn_raw_buffer_store_b128(lo, out.r, (int)at, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(hi, out.r, (int)at + 16, 0, 0);
   } else if constexpr (!BF16 && OUT_BF16) {
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
     const u32x2 w = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
@@ -318,9 +321,12 @@ __host__ __device__ inline int hold_vectors(int nvec) {
   return H * T + (more > 0 ? (more + U * T - 1) / (U * T) * (U * T) : 0);
 }
 
-// One workgroup of T threads per row; H vectors per thread stay in registers. GRAD false: the forward
-// call, nothing held.
-template <bool BF16, bool OUT_BF16, bool GRAD, int T, int H>
+// The call that a kernel serves: loss, statistics and gradient at once, or either part.
+enum Call : int { kFused = 0, kFwd = 1, kBwd = 2 };
+
+// One workgroup of T threads per row; H vectors per thread are loaded at once and stay
+// in registers.
+template <bool BF16, bool OUT_BF16, int CALL, int T, int H>
 __global__ void __launch_bounds__(T) k_topk_loss_hold(TopkLossParams P) {
   using V = Vec<BF16>;
   constexpr int EPV = V::EPV;
@@ -337,42 +343,46 @@ __global__ void __launch_bounds__(T) k_topk_loss_hold(TopkLossParams P) {
   clear_bitmap<EPV, T>(listed, 0, hold_vectors<T, H, U>(nvec), P.vocab);
   lds_barrier();
   List li;
-  if (tid < 64) read_list<BF16>(P, S, listed, row, true, li);
-  lds_barrier();
-  Rest rest;
+  if (tid < 64) read_list<BF16>(P, S, listed, row, CALL != kBwd, li);
+  if constexpr (CALL == kBwd) {
+    if (tid < 64) row_classes(P, S, row, li, P.row_stats[4 * (int64_t)row], P.row_stats[4 * (int64_t)row + 1], false);
+  } else {
+    lds_barrier();
+    Rest rest;
 #pragma unroll
-  for (int i = 0; i < H; ++i)
-    if (i * T < nvec) {
-      float x[EPV];
-      V::unpack(held[i], x);
-      rest.add<EPV>(x, listed_bits<EPV>(listed, i * T + tid));
-      settle(held[i], rest);
+    for (int i = 0; i < H; ++i)
+      if (i * T < nvec) {
+        float x[EPV];
+        V::unpack(held[i], x);
+        rest.add<EPV>(x, listed_bits<EPV>(listed, i * T + tid));
+        settle(held[i], rest);
+      }
+    for (int v0 = H * T; v0 < nvec; v0 += U * T) {
+      u32x4 raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) raw[u] = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)(v0 + u * T) * 16u);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float x[EPV];
+        V::unpack(raw[u], x);
+        rest.add<EPV>(x, listed_bits<EPV>(listed, v0 + u * T + tid));
+        settle(raw[u], rest);
+      }
     }
-  for (int v0 = H * T; v0 < nvec; v0 += U * T) {
-    u32x4 raw[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) raw[u] = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)(v0 + u * T) * 16u);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float x[EPV];
-      V::unpack(raw[u], x);
-      rest.add<EPV>(x, listed_bits<EPV>(listed, v0 + u * T + tid));
-      settle(raw[u], rest);
+    wave_lse(rest.ref, rest.sum);
+    if ((tid & 63) == 0) {
+      S.part[tid >> 6][0] = rest.ref;
+      S.part[tid >> 6][1] = rest.sum;
+    }
+    lds_barrier();
+    if (tid < 64) {
+      float ref = tid < T / 64 ? S.part[tid][0] : kNoRef;
+      float sum = tid < T / 64 ? S.part[tid][1] : 0.f;
+      wave_lse(ref, sum);
+      row_classes(P, S, row, li, ref, sum > 0.f ? lg2(sum) : kNegInf, true);
     }
   }
-  wave_lse(rest.ref, rest.sum);
-  if ((tid & 63) == 0) {
-    S.part[tid >> 6][0] = rest.ref;
-    S.part[tid >> 6][1] = rest.sum;
-  }
-  lds_barrier();
-  if (tid < 64) {
-    float ref = tid < T / 64 ? S.part[tid][0] : kNoRef;
-    float sum = tid < T / 64 ? S.part[tid][1] : 0.f;
-    wave_lse(ref, sum);
-    row_classes(P, S, row, li, ref, sum > 0.f ? lg2(sum) : kNegInf, true);
-  }
-  if constexpr (GRAD) {
+  if constexpr (CALL != kFwd) {
     lds_barrier();
     const float L = S.L, factor = S.factor;
     uint8_t* dr = P.dz + (int64_t)row * P.ld_dz_bytes;
@@ -521,11 +531,18 @@ __global__ void __launch_bounds__(kThreads) k_topk_loss_grad(TopkLossParams P) {
 
 // Rows from which a workgroup per row is faster than segments of rows. Fused (151936 bf16): 96 rows 25 us
 // whole, 18 split, 192 rows 31 and 37. The forward call alone: 128 rows of 151936 fp32 logits 28 us whole,
-// 23.5 split, 192 rows 29 and 31; rows of up to 8192 vectors are faster whole at any number (50257 bf16,
-// 16 rows: 8.5 and 9 to 10 us), as the split call has a second launch.
+// 23.5 split, 192 rows 26 and 31; rows of up to 8192 vectors are faster whole at any number (50257 bf16,
+// 16 rows: 8.5 and 9 to 10 us), as the split call has a second launch. Its threads begin with four or
+// eight vectors each and stream the rest; 1024 of them to a long row (8192 rows of 151936 bf16 386 us, 420
+// with 512), 256 to a short one (8192 rows of 8192 bf16 32 us, 44 with 512).
 constexpr int kHoldRows = 128;
 constexpr int kHoldRowsFwd = 160;
 constexpr int kWholeVecFwd = 8192;
+// The backward call, which every segment's workgroup begins with the row's classes: 128 rows of 151936
+// bf16 18 us whole, 15 in segments, 256 rows 29 and 33, 2048 rows 215 and 253. Of rows of medium length 512
+// threads hold eight vectors each (2048 rows of 100003 bf16, fp32 gradient: 314 us, 348 with 19).
+constexpr int kHoldRowsBwd = 256;
+constexpr int kShortVecBwd = 16384;
 // Workgroups of segments that few rows are split for: more of them read the lists and join the sums once
 // more (16 rows of 151936 bf16 fused 10.8 us, with 512 workgroups 12.1, with 1024 15.8).
 constexpr int kSplitGroups = 256;
@@ -552,9 +569,9 @@ hipError_t launch_with_bitmap(K kernel, dim3 grid, int threads, int vectors, int
   return hipGetLastError();
 }
 
-template <bool BF16, bool OUT_BF16, bool GRAD, int T, int H>
+template <bool BF16, bool OUT_BF16, int CALL, int T, int H>
 hipError_t launch_hold(const TopkLossParams& p, hipStream_t s) {
-  return launch_with_bitmap(k_topk_loss_hold<BF16, OUT_BF16, GRAD, T, H>, dim3((unsigned)p.n_rows), T,
+  return launch_with_bitmap(k_topk_loss_hold<BF16, OUT_BF16, CALL, T, H>, dim3((unsigned)p.n_rows), T,
                             hold_vectors<T, H, kLoose>(p.nvec), Vec<BF16>::EPV, p, s);
 }
 
@@ -570,21 +587,35 @@ hipError_t launch_sums(const TopkLossParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <bool BF16, bool OUT_BF16, int CALL>
+hipError_t launch_long(const TopkLossParams& p, hipStream_t s) {
+  if (p.nvec > 512 * 19 && (p.n_rows <= kOneEach || p.nvec > kHoldVec))
+    return launch_hold<BF16, OUT_BF16, CALL, 1024, 19>(p, s);
+  return launch_hold<BF16, OUT_BF16, CALL, 512, 19>(p, s);
+}
+
 template <bool BF16, bool OUT_BF16>
 hipError_t launch_fused(const TopkLossParams& p, hipStream_t s) {
-  if (p.n_rows >= kHoldRows) {
-    if (p.nvec <= 256 * 16) return launch_hold<BF16, OUT_BF16, true, 256, 16>(p, s);
-    if (p.nvec > 512 * 19 && (p.n_rows <= kOneEach || p.nvec > kHoldVec))
-      return launch_hold<BF16, OUT_BF16, true, 1024, 19>(p, s);
-    return launch_hold<BF16, OUT_BF16, true, 512, 19>(p, s);
-  }
+  if (p.n_rows >= kHoldRows)
+    return p.nvec <= 256 * 16 ? launch_hold<BF16, OUT_BF16, kFused, 256, 16>(p, s)
+                              : launch_long<BF16, OUT_BF16, kFused>(p, s);
   const hipError_t e = launch_sums<BF16>(p, s);
   return e != hipSuccess ? e : launch_grad<BF16, OUT_BF16, true>(p, s);
 }
 
+template <bool BF16, bool OUT_BF16>
+hipError_t launch_bwd(const TopkLossParams& p, hipStream_t s) {
+  if (p.n_rows >= kHoldRowsBwd && p.nvec > kSegVec)
+    return p.nvec <= kShortVecBwd ? launch_hold<BF16, OUT_BF16, kBwd, 512, 8>(p, s)
+                                  : launch_long<BF16, OUT_BF16, kBwd>(p, s);
+  return launch_grad<BF16, OUT_BF16, false>(p, s);
+}
+
 template <bool BF16>
 hipError_t launch_fwd(const TopkLossParams& p, hipStream_t s) {
-  if (p.n_rows >= kHoldRowsFwd || p.nvec <= kWholeVecFwd) return launch_hold<BF16, false, false, 512, 0>(p, s);
+  if (p.nvec <= 256 * 8) return launch_hold<BF16, false, kFwd, 256, 8>(p, s);
+  if (p.nvec <= kWholeVecFwd) return launch_hold<BF16, false, kFwd, 512, 4>(p, s);
+  if (p.n_rows >= kHoldRowsFwd) return launch_hold<BF16, false, kFwd, 1024, 4>(p, s);
   const hipError_t e = launch_sums<BF16>(p, s);
   if (e != hipSuccess) return e;
   return launch_with_bitmap(k_topk_loss_row<BF16>, dim3((unsigned)p.n_rows), 64, p.nvec, Vec<BF16>::EPV, p, s);
@@ -613,8 +644,8 @@ hipError_t launch_topk_loss_fwd(const TopkLossParams& p, int in_bf16, hipStream_
 }
 
 hipError_t launch_topk_loss_bwd(const TopkLossParams& p, int in_bf16, int out_bf16, hipStream_t s) {
-  if (in_bf16) return out_bf16 ? launch_grad<true, true, false>(p, s) : launch_grad<true, false, false>(p, s);
-  return out_bf16 ? launch_grad<false, true, false>(p, s) : launch_grad<false, false, false>(p, s);
+  if (in_bf16) return out_bf16 ? launch_bwd<true, true>(p, s) : launch_bwd<true, false>(p, s);
+  return out_bf16 ? launch_bwd<false, true>(p, s) : launch_bwd<false, false>(p, s);
 }
 
 hipError_t launch_topk_loss_fused(const TopkLossParams& p, int in_bf16, int out_bf16, hipStream_t s) {
