@@ -12,12 +12,14 @@
 // all of the row; where the bound turns out to be no reference for it (all others so far below that their
 // terms vanish), the segment is gone over once more for the sum alone.
 //
-// When list or buffer would run over (rows of equal values; rising rows), the vectors in question are gone
-// over in order, the buffer is cut to the k largest and the bound raised to the k-th as often as needed.
+// When list or buffer run over (rows of equal or rising values, masks that leave fewer tokens than the list
+// has places), as many vectors as there are threads are taken in parts, the buffer being cut to the k
+// largest and the bound raised to the k-th, and the rest of the group is gone over again past that bound
+// (256 rows of 151936 bf16 logits, k 64: 28 us; with 20 tokens left by a mask 77 us, all equal 67 us).
 //
 // Results are the same bits every time: every set depends on the data alone, sums are taken in a fixed
 // order, and the terms of listed vectors and of candidates that are left over, which come in any order,
-// are added as whole multiples of 2^-45 of their reference.
+// are added as whole multiples of 2^-48 of their reference.
 //
 // This file is compiled with the IEEE mode off, like the row kernels: NaN is outside the contract.
 
@@ -35,9 +37,9 @@ constexpr int kLoose = 4;        // vectors in flight per thread of what is not 
 constexpr int kGroup = 4;        // times those between two looks at the list
 constexpr int kBatch = 128;      // threads that append between two checks where the buffer runs over
 constexpr int kListMost = 1024;  // vectors with candidates between two looks at them
-constexpr int kSearchMost = 1024;  // candidates up to which one wave's search beats sorting all of them
-constexpr int kSortedMost = 512;
-constexpr float kUnit = 0x1p45f; // one over the unit of the sums that are taken in any order
+constexpr int kWaveMost = 1024;  // candidates that one wave searches
+constexpr int kRankMost = 512;   // keys that are ranked by counting, one thread each
+constexpr float kUnit = 0x1p48f; // one over the unit of the sums that are taken in any order
 constexpr float kLeastSum = 0x1p-16f;  // least sum, relative to its reference, that these units are fine enough for
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
 
@@ -91,15 +93,16 @@ __device__ __forceinline__ void settle(u32x4& v, Low& low) { asm volatile("" : "
 
 struct Shared {
   uint64_t keys[kTopkCap];
-  uint64_t sorted[kSortedMost];
+  uint64_t sorted[kRankMost];
   u32x4 listed_raw[kListMost];
   uint32_t list[kListMost];
   uint32_t maxima[512];
   uint64_t units[16][2];
   float pair[16][2];
   float bound;
-  uint32_t least;  // the search's result
-  int count, listed, n_sorted;
+  uint64_t least;  // the search's result
+  int count, listed, n_sorted, reach;
+  int tally[3];
   int again;  // the sum has to be formed anew
 };
 
@@ -152,28 +155,6 @@ __device__ void flush(Shared& S, const Low& low, const Left& left, bool last, Re
   lds_barrier();
 }
 
-// Sorts n keys, the largest first; room for the next power of two from `least` on. All threads.
-template <int T>
-__device__ void sort_keys(uint64_t* keys, int n, int least) {
-  const int tid = thread_x();
-  int m = least;
-  while (m < n) m <<= 1;
-  for (int i = n + tid; i < m; i += T) keys[i] = 0;
-  lds_barrier();
-  for (int size = 2; size <= m; size <<= 1)
-    for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      for (int i = tid; i < m / 2; i += T) {
-        const int a = 2 * i - (i & (stride - 1)), b = a + stride;
-        const uint64_t x = keys[a], y = keys[b];
-        if ((x < y) == ((a & size) == 0)) {
-          keys[a] = y;
-          keys[b] = x;
-        }
-      }
-      lds_barrier();
-    }
-}
-
 // The first bound: the k-th largest of m maxima' keys in S.maxima (one wave; m a multiple of 64), as far as
 // its upper `bits` bits say, rounded down; -inf where there are not k.
 template <int M>
@@ -193,10 +174,10 @@ __device__ void find_bound(Shared& S, int k, int bits) {
   if (lane == 0) S.bound = key_value(max(p, kKeyNegInf));
 }
 
-// The largest 32-bit number that at least k of the n > k keys' upper halves reach, or a smaller one that
-// exactly k reach. One wave; R: keys per lane.
+// A number that the upper halves of at least k of the n > k keys reach: bits are decided one by one, from the
+// highest, until exactly k are left, or more that share the k-th's upper half. One wave; R: keys per lane.
 template <int R>
-__device__ void search_keys(Shared& S, int n, int k) {
+__device__ __forceinline__ void search_keys(Shared& S, int n, int k) {
   const int lane = thread_x() & 63;
   uint32_t key[R];
   uint32_t top = 0, bottom = ~0u;
@@ -212,89 +193,107 @@ __device__ void search_keys(Shared& S, int n, int k) {
   // the bits that all have in common need no search
   int b = top == bottom ? -1 : 31 - __builtin_clz(top ^ bottom);
   uint32_t p = b < 0 ? top : b == 31 ? 0u : top >> (b + 1) << (b + 1);
+  int reach = n;
   for (; b >= 0; --b) {
     const uint32_t q = p | (1u << b);
     int c = 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[i] >= q));
-    if (c >= k) p = q;
+    if (c >= k) {
+      p = q;
+      reach = c;
+    }
     if (c == k) break;
   }
   if (lane == 0) {
-    S.least = p;
-    S.n_sorted = 0;
+    S.least = (uint64_t)p << 32;
+    S.reach = reach;
   }
 }
 
-// Cuts the n keys in S.keys to the k largest, in order; those left over go to `left`, or to `rest` in the
-// order of their rank. Returns the number kept; S.bound is the k-th's value. All T threads call it.
+// The k-th largest of n > k keys, by all threads: where one wave does not hold them, or too many upper
+// halves are the same. A barrier a bit; the counts go round three places, one of them being cleared.
 template <int T>
-__device__ int cut(Shared& S, int n, int k, Left& left, Rest& rest) {
+__device__ __forceinline__ uint64_t search_wide(Shared& S, int n, int k) {
+  constexpr int R = kTopkCap / T;
   const int tid = thread_x();
+  uint64_t key[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) key[i] = i * T + tid < n ? S.keys[i * T + tid] : 0;
+  if (tid < 2) S.tally[tid] = 0;
+  lds_barrier();
+  uint64_t p = 0;
+  int at = 0;
+  for (int b = 63; b >= 0; --b) {
+    const uint64_t q = p | (1ull << b);
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[i] >= q));
+    if ((tid & 63) == 0 && c) atomicAdd(&S.tally[at], c);
+    lds_barrier();
+    c = S.tally[at];
+    if (tid == 0) S.tally[at == 0 ? 2 : at - 1] = 0;
+    at = at == 2 ? 0 : at + 1;
+    if (c >= k) p = q;
+    if (c == k) break;
+  }
+  lds_barrier();
+  return p;
+}
+
+// Cuts the n keys in S.keys to the k largest, in order; those left over go to `left`. Returns the number
+// kept; S.bound is the k-th's value. All T threads call it.
+template <int T>
+__device__ __forceinline__ int cut(Shared& S, int n, int k, Left& left) {
+  const int tid = thread_x();
+  constexpr int kMost = T < kRankMost ? T : kRankMost;
   const uint64_t* from = S.keys;
   int m = n;  // keys that are put in order
-  bool searched = false;
   left = Left{};
   auto leave = [&](uint64_t key) {
     left.units += (uint64_t)(ex2(__builtin_fmaf(key_value((uint32_t)(key >> 32)), kLog2e, -left.ref)) * kUnit);
   };
-  if (n > k && n <= kSearchMost) {
-    if (tid < 64) {
-      if (n <= 256)
-        search_keys<4>(S, n, k);
-      else
-        search_keys<kSearchMost / 64>(S, n, k);
+  if (n > k) {
+    if (tid == 0) S.n_sorted = 0;
+    if (n <= kWaveMost) {
+      if (tid < 64) {
+        if (n <= 256)
+          search_keys<4>(S, n, k);
+        else
+          search_keys<kWaveMost / 64>(S, n, k);
+      }
+      lds_barrier();
     }
-    lds_barrier();
-    const uint32_t least = S.least;
-    left.ref = fmaxf(key_value(max(least, kKeyNegInf)) * kLog2e, kNoRef);
+    const uint64_t least = n > kWaveMost || S.reach > kMost ? search_wide<T>(S, n, k) : S.least;
+    left.ref = fmaxf(key_value(max((uint32_t)(least >> 32), kKeyNegInf)) * kLog2e, kNoRef);
     for (int i = tid; i < n; i += T) {
       const uint64_t key = S.keys[i];
-      if ((uint32_t)(key >> 32) >= least) {
-        const int at = atomicAdd(&S.n_sorted, 1);
-        if (at < kSortedMost) S.sorted[at] = key;
-      } else {
+      if (key >= least)
+        S.sorted[atomicAdd(&S.n_sorted, 1)] = key;
+      else
         leave(key);
-      }
     }
     lds_barrier();
     m = S.n_sorted;
-    searched = m <= kSortedMost;
-    if (searched) {
-      from = S.sorted;
-    } else {  // many equal values: all of them in order after all
-      m = n;
-      left = Left{};
-    }
-  }
-  constexpr int kRankMost = T < kSortedMost ? T : kSortedMost;  // one thread per key
-  if (m <= kRankMost) {
-    uint64_t mine = 0;
-    int rank = 0;
-    if (tid < m) {
-      mine = from[tid];
-#pragma unroll 8
-      for (int j = 0; j < m; ++j) rank += from[j] > mine ? 1 : 0;
-    }
-    lds_barrier();
-    if (tid < m) S.sorted[rank] = mine;
-    lds_barrier();
     from = S.sorted;
-  } else {
-    sort_keys<T>(const_cast<uint64_t*>(from), m, 256);
   }
-  for (int i = k + tid; i < m; i += T) {
-    if (searched)
-      leave(from[i]);
-    else
-      rest.add(key_value((uint32_t)(from[i] >> 32)));
+  uint64_t mine = 0;
+  int rank = 0;
+  if (tid < m) {
+    mine = from[tid];
+#pragma unroll 8
+    for (int j = 0; j < m; ++j) rank += from[j] > mine ? 1 : 0;
   }
+  lds_barrier();
   const int kept = min(n, k);
-  if (from != S.keys)
-    for (int i = tid; i < kept; i += T) S.keys[i] = from[i];
+  if (tid < m) {
+    if (rank < k) S.keys[rank] = mine;
+    else leave(mine);
+    if (rank == k - 1) S.bound = key_value((uint32_t)(mine >> 32));
+  }
   if (tid == 0) {
     S.count = kept;
-    S.bound = n >= k ? key_value((uint32_t)(from[k - 1] >> 32)) : kNegInf;
+    if (n < k) S.bound = kNegInf;
   }
   lds_barrier();
   return kept;
@@ -364,7 +363,7 @@ __device__ void take_again(Shared& S, float& bound, float was, const Low& none, 
   for (int b = 0; b < T / kBatch; ++b) {
     if (n + kBatch * EPV > kTopkCap) {
       Left left;
-      n = cut<T>(S, n, k, left, rest);
+      n = cut<T>(S, n, k, left);
       if (n == k) bound = bound_after_cut(S.bound);
       flush<T>(S, none, left, false, rest);
     }
@@ -387,7 +386,7 @@ __device__ void take_again(Shared& S, float& bound, float was, const Low& none, 
 // One workgroup of T threads per (row, segment); H vectors per thread are held. M: maxima that the first
 // bound is found from.
 template <bool BF16, int T, int H, int M>
-__global__ void __launch_bounds__(T) k_topk(TopkParams P) {
+__global__ void __launch_bounds__(T, T == 512 ? 6 : 3) k_topk(TopkParams P) {
   using V = Vec<BF16>;
   constexpr int EPV = V::EPV;
   constexpr int U = kLoose;
@@ -449,9 +448,22 @@ __global__ void __launch_bounds__(T) k_topk(TopkParams P) {
     }
   });
   // Vectors [g0, g1) are gone over between two looks at the list: the held ones, then kGroup * U per thread.
+  // After the list ran over, those among them at or above `seen` once more, past a higher bound.
   int n = 0, g0 = 0, g1 = H * T;
+  float seen = kNegInf;
+  bool held_ones = true, again = false;
   for (;;) {
-    if (g0 > 0)
+    if (again) {
+      for (int v = g0; v < g1 && v < n_vec; v += T) {
+        u32x4 raw = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)v * 16u);
+        float x[EPV];
+        unpack(raw, v, x);
+        float top = x[0];
+#pragma unroll
+        for (int e = 1; e < EPV; ++e) top = fmaxf(top, x[e]);
+        if (top >= seen) take<EPV>(S, bound, low, raw, x, v + tid);
+      }
+    } else if (!held_ones) {
       for (int v = g0; v < g1 && v < n_vec; v += U * T) {
         u32x4 raw[U];
         each<U>([&](auto u) { raw[u] = buf_load16<kStream>(in, (uint32_t)tid * 16u, (uint32_t)(v + u * T) * 16u); });
@@ -462,7 +474,8 @@ __global__ void __launch_bounds__(T) k_topk(TopkParams P) {
           settle(raw[u], low);
         });
       }
-    const bool last = g1 >= n_vec;
+    }
+    held_ones = false;
     lds_barrier();
     const int listed = S.listed;
     int total = n;
@@ -494,23 +507,32 @@ __global__ void __launch_bounds__(T) k_topk(TopkParams P) {
       if (!fits) S.count = n;
     }
     const float was = bound;
+    Left left;
     if (fits) {
       n = total;
       low = more;
+      g0 = g1;
+      again = false;
       lds_barrier();
     } else {
-      // back to the keys of before, and those vectors in order
+      // back to the keys of before; the first T vectors in parts, the others past what these make the bound
       lds_barrier();
-      for (int v = g0; v < g1 && v < n_vec; v += T) {
-        u32x4 raw = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)v * 16u);
-        float x[EPV];
-        unpack(raw, v, x);
-        take_again<EPV, T>(S, bound, was, Low{low.ref}, rest, x, base + (v + tid) * EPV, end, n, k);
-      }
+      u32x4 raw = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)g0 * 16u);
+      float x[EPV];
+      unpack(raw, g0, x);
+      take_again<EPV, T>(S, bound, fmaxf(was, seen), Low{low.ref}, rest, x, base + (g0 + tid) * EPV, end, n, k);
+      seen = was;
+      again = true;
+      g0 += T;
     }
-    Left left;
-    if (last || n > kTopkCap / 2) {
-      n = cut<T>(S, n, k, left, rest);
+    const bool last = g0 >= n_vec;
+    if (g0 >= g1) {
+      again = false;
+      g1 = g0 + kGroup * U * T;
+    }
+    if (!again) seen = kNegInf;
+    if (last || n > kTopkCap / 2 || (!fits && n > k)) {
+      n = cut<T>(S, n, k, left);
       if (n == k && !last) bound = bound_after_cut(S.bound);
     }
     if (last || bound != was) {  // (a sum to which a higher bound's will be added need not be fine)
@@ -518,15 +540,15 @@ __global__ void __launch_bounds__(T) k_topk(TopkParams P) {
       low.rebase(bound);
     }
     if (last) break;
-    g0 = g1;
-    g1 += kGroup * U * T;
   }
   const int kept = n;
   if (S.again) {
-    // The bound was no reference for the sum: the others again, by themselves.
+    // The bound was no reference for the sum: the others again, by themselves (none has weight if the list
+    // already ends in -inf, or is not full).
     rest = Rest{};
     const uint64_t least = kept == k ? S.keys[k - 1] : 0;
-    for (int v = 0; v < n_vec; v += T) {
+    const int n_again = (uint32_t)(least >> 32) > kKeyNegInf ? n_vec : 0;
+    for (int v = 0; v < n_again; v += T) {
       u32x4 raw = buf_load16<kCached>(in, (uint32_t)tid * 16u, (uint32_t)v * 16u);
       float x[EPV];
       unpack(raw, v, x);
@@ -584,8 +606,7 @@ __global__ void __launch_bounds__(kThreads) k_topk_merge(TopkParams P) {
   const int n = S.count;
   lds_barrier();
   Left left;
-  Rest none;
-  const int kept = cut<T>(S, n, k, left, none);
+  const int kept = cut<T>(S, n, k, left);
   const uint64_t least = kept == k ? S.keys[k - 1] : 0;
 #pragma unroll
   for (int i = 0; i < R; ++i)

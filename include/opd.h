@@ -393,8 +393,9 @@ opd_status_t opd_topk_rows(const void* y, opd_dtype_t dt, int64_t n_rows, int64_
  *   dz         [n_rows, ld_dz] of dtype dz_dt, every token's (up to vocab); must not overlap z.
  *   scratch    device memory of at least opd_topk_loss_scratch_size(n_rows, vocab, dt) bytes (may be
  *              0), 16-byte aligned; not shared by calls that run at once. The backward call needs none.
- * The fused call gives the forward's and the backward's outputs, and z is read from HBM once where the
- * rows' working set fits the chip. Separate and fused calls agree to rounding, not bit for bit.
+ * The fused call gives the forward's and the backward's outputs; what a row's workgroups do not hold of z
+ * between its sum and its gradient they read a second time. Separate and fused calls agree to rounding,
+ * not bit for bit.
  * Errors: OPD_ERR_NULL, OPD_ERR_SHAPE (k too), OPD_ERR_DTYPE, OPD_ERR_ALIGN, OPD_ERR_PARAM (alpha, tau, kl),
  * OPD_ERR_WORKSPACE, OPD_ERR_HIP.
  */
