@@ -34,7 +34,7 @@ namespace opd {
 namespace {
 
 constexpr int kLoose = 4;        // vectors in flight per thread of what is not held
-constexpr int kGroup = 4;        // times those between two looks at the list
+constexpr int kGroup = 8;        // times those between two looks at the list
 constexpr int kBatch = 128;      // threads that append between two checks where the buffer runs over
 constexpr int kListMost = 1024;  // vectors with candidates between two looks at them
 constexpr int kWaveMost = 1024;  // candidates that one wave searches
