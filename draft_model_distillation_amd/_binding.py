@@ -183,10 +183,16 @@ def _check(fn: str, status: int):
 # ------------------------------------------------------------------ torch-facing helpers
 
 
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
@@ -206,18 +212,21 @@ def _matrix(t, name: str, whole_vectors: bool = True):
     the last element only (whole_vectors=False)."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D [rows, vocab]")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if cols > 1 and unit != 1:
         raise ValueError(f"{name} must have unit stride along the vocabulary")
-    ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-    if ld < t.shape[1]:
-        raise ValueError(f"{name}: row pitch {ld} is shorter than a row ({t.shape[1]})")
-    if t.shape[0] > 0 and t.shape[1] > 0 and t.device.type != "meta":
-        per = max(1, 16 // t.element_size()) if whole_vectors else 1
-        last = ((t.shape[1] + per - 1) // per) * per
-        span = (t.storage_offset() + (t.shape[0] - 1) * ld + last) * t.element_size()
-        if span > t.untyped_storage().nbytes():
+    if rows <= 1:
+        ld = max(ld, cols)
+    if ld < cols:
+        raise ValueError(f"{name}: row pitch {ld} is shorter than a row ({cols})")
+    if rows > 0 and cols > 0 and t.device.type != "meta":
+        size = t.element_size()
+        per = max(1, 16 // size) if whole_vectors else 1
+        last = ((cols + per - 1) // per) * per
+        if (t.storage_offset() + (rows - 1) * ld + last) * size > t.untyped_storage().nbytes():
             raise ValueError(f"{name}: the storage ends before the last row's last 16-byte vector")
-    return t.data_ptr(), t.shape[0], t.shape[1], ld
+    return t.data_ptr(), rows, cols, ld
 
 
 # ------------------------------------------------------------------ argument validation
@@ -771,12 +780,11 @@ def _on_device(f):
 
 def _stream_and_workspace(dev, ws):
     """The device's current stream (its handle) and the workspace to use on it."""
-    st = _torch().cuda.current_stream(dev)
-    handle = st.cuda_stream
+    handle = _torch()._C._cuda_getCurrentRawStream(dev.index)  # (a stream object costs ten times as long)
     if ws is None:
         ws = _ws_cache.get((dev.type, dev.index, handle))
         if ws is None:
-            ws = workspace(dev, st)
+            ws = workspace(dev)
     else:
         _workspace_arg(ws, dev)
     return handle, ws
