@@ -340,6 +340,19 @@ opd_status_t finish(opd_status_t s, void* ws, hipStream_t stream) {
   return fail(OPD_ERR_DEVICE, std::string(head) + flag_text(v));
 }
 
+// Calls launch(first row, rows) for parts of at most kMostRows rows: a grid's threads have to be countable in
+// 32 bits. The parts are of nearly equal size, so that none of many rows is launched like one of few.
+template <class F>
+hipError_t in_parts(int64_t n_rows, F launch) {
+  constexpr int64_t kMostRows = 1 << 21;  // workgroups have up to 1024 threads
+  const int64_t parts = (n_rows + kMostRows - 1) / kMostRows, per = (n_rows + parts - 1) / parts;
+  for (int64_t r = 0; r < n_rows; r += per) {
+    const hipError_t e = launch(r, (int32_t)std::min(per, n_rows - r));
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 }  // namespace
 
 namespace opd {
@@ -635,8 +648,8 @@ static opd_status_t opd_adjust_logits_impl(const void* x, opd_dtype_t dt, int64_
   if (a->n_blocks < 0) return fail(OPD_ERR_SHAPE, "n_blocks must be >= 0");
   if (a->n_blocks > 0 && !a->offsets) return fail(OPD_ERR_NULL, "offsets must be non-NULL");
   if (a->history) {
-    if (a->max_history < 0 || a->ld_history < a->max_history)
-      return fail(OPD_ERR_SHAPE, "ld_history must be >= max_history >= 0");
+    if (a->max_history < 0 || a->max_history > opd::kMaxHistory || a->ld_history < a->max_history)
+      return fail(OPD_ERR_SHAPE, "max_history must be in [0, 2^30] and ld_history >= max_history");
     if (a->n_blocks > 0 && !a->history_len) return fail(OPD_ERR_NULL, "history needs history_len");
   }
   if (a->bias_tokens || a->bias_values) {
@@ -697,6 +710,20 @@ static opd_status_t check_scratch(const void* scratch, size_t bytes, size_t need
   return OPD_OK;
 }
 
+// The parameters of rows [r, r + n) of a call (one that is launched in parts uses no scratch).
+static opd::TopkLossParams loss_part(opd::TopkLossParams p, int64_t r, int32_t n) {
+  p.n_rows = n;
+  p.z += r * p.ld_bytes;
+  p.top_index += r * p.k;
+  p.top_logit += r * p.k;
+  if (p.rest_lse) p.rest_lse += r;
+  if (p.grad_loss) p.grad_loss += r;
+  if (p.loss) p.loss += r;
+  p.row_stats += 4 * r;
+  if (p.dz) p.dz += r * p.ld_dz_bytes;
+  return p;
+}
+
 size_t opd_topk_scratch_size(int64_t n_rows, int64_t vocab, opd_dtype_t dt, int32_t k) {
   if (n_rows <= 0 || n_rows > INT32_MAX || vocab <= 0 || vocab > kMaxVocab || !valid_dtype(dt) || k < 1 ||
       k > opd::kTopkMax)
@@ -735,7 +762,15 @@ static opd_status_t opd_topk_rows_impl(const void* y, opd_dtype_t dt, int64_t n_
     p.seg_keys = static_cast<uint64_t*>(scratch);
     p.seg_lse = reinterpret_cast<float*>(p.seg_keys + (size_t)n_rows * p.n_seg * k);
   }
-  hipError_t e = opd::launch_topk(p, dt == OPD_BF16, stream);
+  hipError_t e = in_parts(n_rows, [&](int64_t r, int32_t n) {
+    opd::TopkParams q = p;
+    q.n_rows = n;
+    q.y += r * p.ld_bytes;
+    q.values += r * k;
+    q.index += r * k;
+    q.rest_lse += r;
+    return opd::launch_topk(q, dt == OPD_BF16, stream);
+  });
   if (e != hipSuccess) return hip_fail(e, "top-k kernel launch");
   return OPD_OK;
 }
@@ -795,7 +830,9 @@ static opd_status_t opd_topk_loss_fwd_impl(const void* z, opd_dtype_t dt, int64_
   p.loss = loss;
   p.row_stats = row_stats;
   p.seg_lse = static_cast<float*>(scratch);
-  hipError_t e = opd::launch_topk_loss_fwd(p, dt == OPD_BF16, stream);
+  hipError_t e = in_parts(n_rows, [&](int64_t r, int32_t n) {
+    return opd::launch_topk_loss_fwd(loss_part(p, r, n), dt == OPD_BF16, stream);
+  });
   if (e != hipSuccess) return hip_fail(e, "top-k loss kernel launch");
   return OPD_OK;
 }
@@ -817,7 +854,9 @@ static opd_status_t opd_topk_loss_bwd_impl(const void* z, opd_dtype_t dt, int64_
   p.grad_loss = grad_loss;
   p.dz = static_cast<uint8_t*>(dz);
   p.ld_dz_bytes = ld_dz * (int64_t)dtype_size(dz_dt);
-  hipError_t e = opd::launch_topk_loss_bwd(p, dt == OPD_BF16, dz_dt == OPD_BF16, stream);
+  hipError_t e = in_parts(n_rows, [&](int64_t r, int32_t n) {
+    return opd::launch_topk_loss_bwd(loss_part(p, r, n), dt == OPD_BF16, dz_dt == OPD_BF16, stream);
+  });
   if (e != hipSuccess) return hip_fail(e, "top-k loss gradient kernel launch");
   return OPD_OK;
 }
@@ -844,7 +883,9 @@ static opd_status_t opd_topk_fused_fwd_bwd_impl(const void* z, opd_dtype_t dt, i
   p.grad_loss = grad_loss;
   p.dz = static_cast<uint8_t*>(dz);
   p.ld_dz_bytes = ld_dz * (int64_t)dtype_size(dz_dt);
-  hipError_t e = opd::launch_topk_loss_fused(p, dt == OPD_BF16, dz_dt == OPD_BF16, stream);
+  hipError_t e = in_parts(n_rows, [&](int64_t r, int32_t n) {
+    return opd::launch_topk_loss_fused(loss_part(p, r, n), dt == OPD_BF16, dz_dt == OPD_BF16, stream);
+  });
   if (e != hipSuccess) return hip_fail(e, "fused top-k loss kernel launch");
   return OPD_OK;
 }

@@ -108,3 +108,60 @@ def test_masked_rows_keep_their_tokens(lib):
             assert np.array_equal(out["index"][r].cpu().numpy(), ri)
             n = min(k, int(allowed[r].sum()))
             assert allowed[r][ri[:n]].all()
+
+
+def test_more_rows_than_a_grid_counts(lib):
+    # 2^24 rows of a workgroup each have more threads than 32 bits count
+    import torch
+
+    R, V = (1 << 24) + 5, 8
+    g = torch.Generator(device="cuda").manual_seed(5)
+    y = torch.randn(R, V, device="cuda", generator=g).bfloat16()
+    out = lib.topk_rows(y, 2)
+    torch.cuda.synchronize()
+    v, i = y.float().topk(2)
+    assert torch.equal(out["values"], v)
+    assert torch.equal(torch.gather(y.float(), 1, out["index"].long()), v)
+    rest = torch.scatter(y.double(), 1, out["index"].long(), -float("inf")).logsumexp(1)
+    assert float((out["rest_lse"].double() - rest).abs().max()) <= GT.U32 * 110  # GT's bound for V = 8 and |rest| < 8
+    w = torch.rand(R, device="cuda", generator=g)
+    args = (y, out["index"], out["values"] * 0.5, out["rest_lse"], 0.7, 0.05)
+    loss, stats = lib.topk_loss_fwd(*args)
+    dz = lib.topk_loss_bwd(*args, stats, grad_loss=w)
+    both = lib.topk_fused_fwd_bwd(*args, grad_loss=w)
+    last = tuple(t[-3:].contiguous() for t in args[:4]) + args[4:]
+    few = lib.topk_fused_fwd_bwd(*last, grad_loss=w[-3:].contiguous())
+    torch.cuda.synchronize()
+    assert float((loss - both["loss"]).abs().max()) <= 1e-5 and float((loss[-3:] - few["loss"]).abs().max()) <= 1e-5
+    # (gradients below 2 that differ by fp32's roundings: to bf16 they round to neighbours, 2^-7 apart, at most)
+    assert float((dz.float() - both["dz"].float()).abs().max()) <= 2.0 ** -7 + 1e-5
+    assert float((dz[-3:].float() - few["dz"].float()).abs().max()) <= 2.0 ** -7 + 1e-5
+
+
+@pytest.mark.parametrize("rows", [3, 130])
+def test_the_widest_rows_replayed(lib, rows):
+    # their bitmap takes more LDS than a kernel has without asking for it
+    import torch
+
+    V = 524288
+    y, z, _ = GL._rows(21, 2, V)
+    pick = np.arange(rows) % 2
+    idx, logit, rest = (torch.from_numpy(a[pick].copy()).cuda() for a in GL._lists(y, 20))
+    zt = torch.from_numpy(z[pick].astype(np.float32)).cuda()
+    eager = lib.topk_fused_fwd_bwd(zt, idx, logit, rest, 0.6, 0.05)
+    torch.cuda.synchronize()
+    want = [eager[n].clone() for n in ("loss", "dz")]
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        lib.topk_fused_fwd_bwd(zt, idx, logit, rest, 0.6, 0.05)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        out = lib.topk_fused_fwd_bwd(zt, idx, logit, rest, 0.6, 0.05)
+    for _ in range(3):
+        out["dz"].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out["loss"], want[0]) and torch.equal(out["dz"], want[1])
+        lib.topk_fused_fwd_bwd(zt, idx, logit, rest, 0.6, 0.05)
+        torch.cuda.synchronize()
