@@ -32,27 +32,34 @@ __device__ __forceinline__ int clamp_len(const int32_t* p, int b, int most, bool
   return min(max(n, 0), most);
 }
 
-// Whether a block's rows have a mask that allows nothing, or a number that is none.
+// Whether a block's rows have a mask that allows nothing, or a number that is none: a wave a row, until a
+// word with a bit is met.
+template <int T>
 __device__ void check_masks(const AdjustParams& P, int start, int nb) {
-  const int tid = threadIdx.x, T = blockDim.x;
+  constexpr int Q = 4;  // words in flight per lane
+  const int lane = threadIdx.x & 63;
+  const int words = (P.vocab + 31) / 32;
+  const uint32_t last = (P.vocab & 31) ? (1u << (P.vocab & 31)) - 1u : ~0u;
   for (int j0 = blockIdx.z * kRowGroup; j0 < nb; j0 += gridDim.z * kRowGroup)
-    for (int j = j0; j < min(j0 + kRowGroup, nb); ++j) {
+    for (int j = j0 + (threadIdx.x >> 6); j < min(j0 + kRowGroup, nb); j += T / 64) {
       const int mr = P.mask_row ? P.mask_row[start + j] : start + j;
       if (mr < 0) continue;
       if (mr >= P.n_masks) {
-        if (tid == 0) atomicOr(P.flags, kFlagBadList);
+        if (lane == 0) atomicOr(P.flags, kFlagBadList);
         continue;
       }
       const uint32_t* m = reinterpret_cast<const uint32_t*>(P.mask + (int64_t)mr * P.ld_mask_bytes);
-      const int words = (P.vocab + 31) / 32;
       bool any = false;
-      for (int w0 = 0; w0 < words && !any; w0 += T) {
-        const int w = w0 + tid;
-        uint32_t bits = w < words ? m[w] : 0u;
-        if (w == words - 1 && (P.vocab & 31)) bits &= (1u << (P.vocab & 31)) - 1u;
-        any = __syncthreads_or(bits != 0u);
+      for (int w0 = 0; w0 < words && !any; w0 += 64 * Q) {
+        uint32_t bits = 0;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const int w = w0 + q * 64 + lane;
+          if (w < words) bits |= m[w] & (w == words - 1 ? last : ~0u);
+        }
+        any = __builtin_amdgcn_ballot_w64(bits != 0u) != 0;
       }
-      if (!any && tid == 0) atomicOr(P.flags, kFlagEmptyMask);
+      if (!any && lane == 0) atomicOr(P.flags, kFlagEmptyMask);
     }
 }
 
@@ -75,7 +82,7 @@ __global__ void __launch_bounds__(T) k_adjust(AdjustParams P) {
     return;
   }
   const int nb = end - start;
-  if ((int)blockIdx.x == P.tiles) return check_masks(P, start, nb);  // the workgroups behind the tiles
+  if ((int)blockIdx.x == P.tiles) return check_masks<T>(P, start, nb);  // the workgroups behind the tiles
   const int v0 = blockIdx.x * P.tile_vec;
   const int nv = min(P.tile_vec, P.nvec - v0);  // vectors of the tile
   const int n_u = (nv + T - 1) / T;
