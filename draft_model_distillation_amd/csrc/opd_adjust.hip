@@ -139,6 +139,14 @@ __global__ void __launch_bounds__(T) k_adjust(AdjustParams P) {
     each<kAhead>([&](auto d) { load(raw[d], bits[d]); });
 
     if constexpr (STATE >= kCounts) {
+      // the first of the lists, in flight while the state is cleared (the buffer ends with the history, word by word)
+      const RowBuf tokens = row_buf(reinterpret_cast<const uint8_t*>(hist), (uint32_t)n_hist * 4u);
+      constexpr int F = 2, Q = 4;  // 16-byte loads of the history in flight per thread: the first, the others
+      u32x4 first[F];
+#pragma unroll
+      for (int q = 0; q < F; ++q) first[q] = buf_load16<kCached>(tokens, (uint32_t)tid * 16u, (uint32_t)(q * T) * 16u);
+      const int first_tok = STATE >= kBiases && tid < n_bias ? btok[tid] : -1;
+      const float first_val = STATE >= kBiases && tid < n_bias ? bval[tid] : 0.f;
       lds_barrier();  // the previous group's rows are done with the state
       const u32x4 zero = {0, 0, 0, 0};
       for (int i = tid; i < n_u * T * EPV / 4; i += T) {
@@ -147,11 +155,12 @@ __global__ void __launch_bounds__(T) k_adjust(AdjustParams P) {
       }
       for (int i = tid; i < kTok / 128; i += T) reinterpret_cast<u32x4*>(prompt)[i] = zero;
       lds_barrier();
+      auto here = [&](int tok) { return (unsigned)tok < (unsigned)P.vocab && (unsigned)(tok - t0) < nt; };
       if constexpr (STATE >= kBiases)  // the last entry of a token counts: the largest number in its slot
         for (int i = tid; i < n_bias; i += T) {
-          const int tok = btok[i];
+          const int tok = i < T ? first_tok : btok[i];
           bad_token |= (unsigned)tok >= (unsigned)P.vocab;
-          if ((unsigned)tok < (unsigned)P.vocab && (unsigned)(tok - t0) < nt) atomicMax(&bias[tok - t0], (uint32_t)i + 1u);
+          if (here(tok)) atomicMax(&bias[tok - t0], (uint32_t)i + 1u);
         }
       // the history, then the proposals of the block's rows before this group
       auto see = [&](int tok, bool in_prompt) {
@@ -164,25 +173,19 @@ __global__ void __launch_bounds__(T) k_adjust(AdjustParams P) {
             atomicAdd(&count[t], 1u);
         }
       };
-      constexpr int Q = 4;  // 16-byte loads in flight per thread
-      struct alignas(4) Four { int32_t t[4]; };  // (of any row pitch)
-      int i = 0;
-      for (; i + 4 * Q * T <= n_hist; i += 4 * Q * T) {
-        Four f[Q];
+      auto see_four = [&](const u32x4& four, int at) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) f[q] = *reinterpret_cast<const Four*>(hist + i + 4 * (q * T + tid));
+        for (int e = 0; e < 4; ++e)
+          if (at + e < n_hist) see((int)four[e], at + e < n_prompt);
+      };
 #pragma unroll
-        for (int q = 0; q < Q; ++q)
+      for (int q = 0; q < F; ++q) see_four(first[q], 4 * (q * T + tid));
+      for (int i = 4 * F * T; i < n_hist; i += 4 * Q * T) {
+        u32x4 f[Q];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) see(f[q].t[e], i + 4 * (q * T + tid) + e < n_prompt);
-      }
-      for (; i < n_hist; i += 4 * T) {
-        int f[4];
+        for (int q = 0; q < Q; ++q) f[q] = buf_load16<kCached>(tokens, (uint32_t)tid * 16u, (uint32_t)(i / 4 + q * T) * 16u);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) f[q] = i + q * T + tid < n_hist ? hist[i + q * T + tid] : t0 + (int)nt;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (i + q * T + tid < n_hist) see(f[q], i + q * T + tid < n_prompt);
+        for (int q = 0; q < Q; ++q) see_four(f[q], i + 4 * (q * T + tid));
       }
       if (P.draft)
         for (int h = tid; h < j0; h += T) see(P.draft[start + h], false);
@@ -191,14 +194,13 @@ __global__ void __launch_bounds__(T) k_adjust(AdjustParams P) {
         uint64_t mine = 0;  // entries tid, tid + T, ... of this thread that count
         int q = 0;
         for (int k = tid; k < n_bias; k += T, ++q) {
-          const int tok = btok[k];
-          if ((unsigned)tok < (unsigned)P.vocab && (unsigned)(tok - t0) < nt && bias[tok - t0] == (uint32_t)k + 1u)
-            mine |= 1ull << q;
+          const int tok = k < T ? first_tok : btok[k];
+          if (here(tok) && bias[tok - t0] == (uint32_t)k + 1u) mine |= 1ull << q;
         }
         lds_barrier();
         q = 0;
         for (int k = tid; k < n_bias; k += T, ++q)
-          if (mine >> q & 1) bias[btok[k] - t0] = __float_as_uint(bval[k]);
+          if (mine >> q & 1) bias[(k < T ? first_tok : btok[k]) - t0] = __float_as_uint(k < T ? first_val : bval[k]);
         lds_barrier();
       }
     }

@@ -649,7 +649,7 @@ static opd_status_t opd_adjust_logits_impl(const void* x, opd_dtype_t dt, int64_
   if (a->n_blocks > 0 && !a->offsets) return fail(OPD_ERR_NULL, "offsets must be non-NULL");
   if (a->history) {
     if (a->max_history < 0 || a->max_history > opd::kMaxHistory || a->ld_history < a->max_history)
-      return fail(OPD_ERR_SHAPE, "max_history must be in [0, 2^30] and ld_history >= max_history");
+      return fail(OPD_ERR_SHAPE, "max_history must be in [0, 2^29] and ld_history >= max_history");
     if (a->n_blocks > 0 && !a->history_len) return fail(OPD_ERR_NULL, "history needs history_len");
   }
   if (a->bias_tokens || a->bias_values) {

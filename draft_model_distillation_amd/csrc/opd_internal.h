@@ -141,7 +141,7 @@ struct SampleParams {
 };
 
 // Penalties, biases and masks on the rows of packed blocks (opd_adjust.hip).
-constexpr int kMaxHistory = 1 << 30;  // tokens of one request's history
+constexpr int kMaxHistory = 1 << 29;  // tokens of one request's history
 constexpr int kMaxBias = 16384;  // entries of one request's bias list
 struct AdjustParams {
   const uint8_t* x;

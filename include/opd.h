@@ -297,7 +297,7 @@ opd_status_t opd_lmhead_fused_fwd_bwd_verify(const void* h, const void* W, int64
  *   offsets          [n_blocks + 1] rows of each request, as in opd_blocks_t.
  *   draft_tokens     [n_rows] proposal of each row, or NULL (rows do not see the block's earlier ones).
  *   history          [n_blocks][ld_history] token of each request, history_len[b] of them (clamped to
- *                    max_history <= 2^30), the first prompt_len[b] being the prompt (NULL: 0, all output);
+ *                    max_history <= 2^29), the first prompt_len[b] being the prompt (NULL: 0, all output);
  *                    NULL: no history.
  *   repetition, frequency, presence  [n_blocks] f32, each NULL for none (1, 0, 0); repetition > 0.
  *   bias_tokens, bias_values  [n_blocks][ld_bias] tokens and f32 values, bias_len[b] of them (clamped

@@ -15,7 +15,7 @@ def lib():
 
 def test_history_longer_than_the_index_range(lib):
     at = dict(history=LV.P, history_len=LV.P, ld_history=1 << 31)
-    assert LV._adjust(lib, **at, max_history=(1 << 30) + 1) == 2
+    assert LV._adjust(lib, **at, max_history=(1 << 29) + 1) == 2
     assert LV._adjust(lib, **at, max_history=(1 << 31) - 1) == 2
     assert "max_history" in lib.opd_last_error().decode()
     assert ctypes.sizeof(B.OpdAdjust) % 8 == 0
