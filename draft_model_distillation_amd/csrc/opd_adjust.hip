@@ -11,6 +11,12 @@
 // number to subtract once per vector, several vectors in flight per thread. The proposals of a block's
 // earlier rows are added on the way, by the thread that holds the token. (A history of H tokens is read by
 // every tile, from the L2: 4 H bytes a tile against 32 KB a row.)
+//
+// Measured: 128 blocks of up to 16 rows of 151936 bf16 logits, a quarter of them masked, histories of up to
+// 4096 tokens 127 us, 5.5 TB/s where a copy reaches 5.1. 61 blocks of 32003 fp32 logits behind up to 65536
+// tokens 57 us, 2.6 TB/s: the scans. 128 single rows with biases 36 us, 2.2 TB/s: every tile's workgroup
+// waits for the row's bounds, the lists' lengths, the lists and the counts in turn, two workgroups to a CU
+// (97 registers); fewer registers or 16-bit counts (half the LDS) do not shorten it. One row 4.2 us.
 
 #include <stdint.h>
 

@@ -39,14 +39,6 @@ __device__ __forceinline__ float lg2(float x) { return __builtin_amdgcn_logf(x);
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ u32x4 load16(const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); }
-__device__ __forceinline__ u32x4 load16_nt(const uint8_t* p) {
-  return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
-}
-__device__ __forceinline__ void store16_nt(uint8_t* p, u32x4 v) {
-  __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
-}
-
 // A row as a buffer resource: loads past `bytes` give 0 and stores there are dropped, so that the threads
 // of a workgroup need no test of their own at the row's end. An address is a byte offset of the lane's and
 // one that is the same in every lane; the latter must not pass the end (the hardware takes it off the

@@ -21,6 +21,12 @@
 // order, and the terms of listed vectors and of candidates that are left over, which come in any order,
 // are added as whole multiples of 2^-48 of their reference.
 //
+// Measured, k 64: 8192 rows of 151936 bf16 logits 410 to 500 us from card to card, 5.0 to 6.1 TB/s (a kernel
+// that only reads: 7.2): the vector ALU is busy 84 % of the time, about half of it with one exp2 an element,
+// which runs at a quarter of the others' rate. 256 rows of 151936 fp32 logits 37 us, 4.2 TB/s: one workgroup to a
+// CU, whose bound, search and ranking nothing hides. 1531 rows of 50257 fp32 logits with k 256 73 us, 4.2
+// TB/s. One row of 151936 bf16, k 20: 12 us in segments and 7 us joining them.
+//
 // This file is compiled with the IEEE mode off, like the row kernels: NaN is outside the contract.
 
 #include <stdint.h>
@@ -34,11 +40,13 @@ namespace opd {
 namespace {
 
 constexpr int kLoose = 4;        // vectors in flight per thread of what is not held
-constexpr int kGroup = 8;        // times those between two looks at the list
+constexpr int kGroup = 8;        // times those between two looks at the list (8192 rows 501 us, with 4 508)
 constexpr int kBatch = 128;      // threads that append between two checks where the buffer runs over
 constexpr int kListMost = 1024;  // vectors with candidates between two looks at them
 constexpr int kWaveMost = 1024;  // candidates that one wave searches
-constexpr int kRankMost = 512;   // keys that are ranked by counting, one thread each
+// Keys that are ranked by counting, one thread each (k 128, 2048 rows of 151936 bf16: 129 us; sorting more than
+// 128 keys by a network took 146).
+constexpr int kRankMost = 512;
 constexpr float kUnit = 0x1p48f; // one over the unit of the sums that are taken in any order
 constexpr float kLeastSum = 0x1p-16f;  // least sum, relative to its reference, that these units are fine enough for
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
