@@ -25,7 +25,7 @@
 // that only reads: 7.2): the vector ALU is busy 84 % of the time, about half of it with one exp2 an element,
 // which runs at a quarter of the others' rate. 256 rows of 151936 fp32 logits 37 us, 4.2 TB/s: one workgroup to a
 // CU, whose bound, search and ranking nothing hides. 1531 rows of 50257 fp32 logits with k 256 73 us, 4.2
-// TB/s. One row of 151936 bf16, k 20: 12 us in segments and 7 us joining them.
+// TB/s. One row of 151936 bf16, k 20: 12 us in segments and 5 us joining them.
 //
 // This file is compiled with the IEEE mode off, like the row kernels: NaN is outside the contract.
 
@@ -581,8 +581,9 @@ __global__ void __launch_bounds__(T, T == 512 ? 6 : 3) k_topk(TopkParams P) {
   }
 }
 
-// One workgroup per row joins the segments' lists and sums: a bound from the threads' maxima, the keys at or
-// above it put in order, the others added to the sums by the threads that loaded them.
+// One workgroup per row joins the segments' lists and sums: of up to a key a thread every one is ranked (16 rows
+// of 151936 bf16, k 1: 12 us with the segments, 14 by way of a bound); of more, those at or above a bound from
+// the threads' maxima are put in order. The others are added to the sums by the threads that loaded them.
 __global__ void __launch_bounds__(kThreads) k_topk_merge(TopkParams P) {
   constexpr int T = kThreads, R = kTopkCap / T;
   __shared__ Shared S;
@@ -601,26 +602,42 @@ __global__ void __launch_bounds__(kThreads) k_topk_merge(TopkParams P) {
     const float* p = P.seg_lse + 2 * ((int64_t)row * P.n_seg + i);
     lse_join(rest.ref, rest.sum, p[0], p[1]);
   }
-  if (tid == 0) S.count = 0;
-  S.maxima[tid] = m;
-  lds_barrier();
-  if (tid < 64) find_bound<T>(S, k, 32);
-  lds_barrier();
-  const float bound = S.bound;
+  if (total <= T) {  // few: every key's rank among all of them
+    S.keys[tid] = mine[0];
+    lds_barrier();
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < total; ++j) rank += S.keys[j] > mine[0] ? 1 : 0;
+    lds_barrier();
+    if (mine[0]) {
+      if (rank < k)
+        S.keys[rank] = mine[0];
+      else
+        rest.add(key_value((uint32_t)(mine[0] >> 32)));
+    }
+    lds_barrier();
+  } else {
+    if (tid == 0) S.count = 0;
+    S.maxima[tid] = m;
+    lds_barrier();
+    if (tid < 64) find_bound<T>(S, k, 32);
+    lds_barrier();
+    const float bound = S.bound;
 #pragma unroll
-  for (int i = 0; i < R; ++i)
-    if (mine[i] && key_value((uint32_t)(mine[i] >> 32)) >= bound) S.keys[atomicAdd(&S.count, 1)] = mine[i];
-  lds_barrier();
-  const int n = S.count;
-  lds_barrier();
-  Left left;
-  const int kept = cut<T>(S, n, k, left);
-  const uint64_t least = kept == k ? S.keys[k - 1] : 0;
+    for (int i = 0; i < R; ++i)
+      if (mine[i] && key_value((uint32_t)(mine[i] >> 32)) >= bound) S.keys[atomicAdd(&S.count, 1)] = mine[i];
+    lds_barrier();
+    const int n = S.count;
+    lds_barrier();
+    Left left;
+    cut<T>(S, n, k, left);
+    const uint64_t least = S.keys[k - 1];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
-    if (mine[i] && mine[i] < least) rest.add(key_value((uint32_t)(mine[i] >> 32)));
+    for (int i = 0; i < R; ++i)
+      if (mine[i] && mine[i] < least) rest.add(key_value((uint32_t)(mine[i] >> 32)));
+  }
   join_rest<T>(S, rest);
-  write_row<T>(P, S, row, kept, rest);
+  write_row<T>(P, S, row, k, rest);  // (the segments hold k keys or more)
 }
 
 // Lists up to this long take the first bound from 256 maxima, longer ones from 512: the bound is the
