@@ -32,6 +32,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "opd_internal.h"
 #include "opd_rows.h"
@@ -41,12 +42,7 @@ namespace {
 
 constexpr int kLoose = 4;        // vectors in flight per thread of what is not held
 constexpr int kGroup = 8;        // times those between two looks at the list (8192 rows 501 us, with 4 508)
-constexpr int kBatch = 128;      // threads that append between two checks where the buffer runs over
-constexpr int kListMost = 1024;  // vectors with candidates between two looks at them
 constexpr int kWaveMost = 1024;  // candidates that one wave searches
-// Keys that are ranked by counting, one thread each (k 128, 2048 rows of 151936 bf16: 129 us; sorting more than
-// 128 keys by a network took 146).
-constexpr int kRankMost = 512;
 constexpr float kUnit = 0x1p48f; // one over the unit of the sums that are taken in any order
 constexpr float kLeastSum = 0x1p-16f;  // least sum, relative to its reference, that these units are fine enough for
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
@@ -99,12 +95,17 @@ struct Low {
 // their sums off together, which costs the registers that the row needs.
 __device__ __forceinline__ void settle(u32x4& v, Low& low) { asm volatile("" : "+v"(v), "+v"(low.sum)); }
 
-struct Shared {
-  uint64_t keys[kTopkCap];
-  uint64_t sorted[kRankMost];
-  u32x4 listed_raw[kListMost];
-  uint32_t list[kListMost];
-  uint32_t maxima[512];
+// What a workgroup has in LDS: CAP candidate keys, a list of LIST vectors, RANK keys that are ranked by counting,
+// one thread each (k 128, 2048 rows of 151936 bf16: 129 us; sorting more than 128 by a network took 146), and
+// as many maxima.
+template <int CAP, int LIST, int RANK>
+struct SharedOf {
+  static constexpr int kCap = CAP, kList = LIST, kRank = RANK;
+  uint64_t keys[CAP];
+  uint64_t sorted[RANK];
+  u32x4 listed_raw[LIST];
+  uint32_t list[LIST];
+  uint32_t maxima[RANK];
   uint64_t units[16][2];
   float pair[16][2];
   float bound;
@@ -113,6 +114,11 @@ struct Shared {
   int tally[3];
   int again;  // the sum has to be formed anew
 };
+// 38 KB, or 22 KB for workgroups of 256 threads, whose rows or segments are short, so that six of those fit a CU
+// (8192 rows of 8000 bf16 logits, k 64: 68 us, with 38 KB 90, with 43 KB 117). With a list of 512 vectors in the
+// larger one k 256 runs over it (1531 rows of 50257 fp32: 117 against 76 us).
+template <int T>
+using Shared = std::conditional_t<T == 256, SharedOf<1024, 512, 256>, SharedOf<kTopkCap, 768, 512>>;
 
 // Sum of whole numbers over the wave, in every lane.
 __device__ __forceinline__ uint64_t wave_sum_units(uint64_t x) {
@@ -137,8 +143,8 @@ struct Left {
 
 // Adds what the threads hold to thread 0's `rest`. A sum that is too small for its units, if it is the last
 // one (`last`) or of candidates, has to be formed anew: S.again. All threads.
-template <int T>
-__device__ void flush(Shared& S, const Low& low, const Left& left, bool last, Rest& rest) {
+template <int T, class SH>
+__device__ void flush(SH& S, const Low& low, const Left& left, bool last, Rest& rest) {
   const int tid = thread_x();
   uint64_t lu = wave_sum_units(left.units), units = wave_sum_units(low.units);
   float sum = wave_sum(low.sum);
@@ -165,8 +171,8 @@ __device__ void flush(Shared& S, const Low& low, const Left& left, bool last, Re
 
 // The first bound: the k-th largest of m maxima' keys in S.maxima (one wave; m a multiple of 64), as far as
 // its upper `bits` bits say, rounded down; -inf where there are not k.
-template <int M>
-__device__ void find_bound(Shared& S, int k, int bits) {
+template <int M, class SH>
+__device__ void find_bound(SH& S, int k, int bits) {
   const int lane = thread_x() & 63;
   uint32_t key[M / 64];
 #pragma unroll
@@ -184,8 +190,8 @@ __device__ void find_bound(Shared& S, int k, int bits) {
 
 // A number that the upper halves of at least k of the n > k keys reach: bits are decided one by one, from the
 // highest, until exactly k are left, or more that share the k-th's upper half. One wave; R: keys per lane.
-template <int R>
-__device__ __forceinline__ void search_keys(Shared& S, int n, int k) {
+template <int R, class SH>
+__device__ __forceinline__ void search_keys(SH& S, int n, int k) {
   const int lane = thread_x() & 63;
   uint32_t key[R];
   uint32_t top = 0, bottom = ~0u;
@@ -221,9 +227,9 @@ __device__ __forceinline__ void search_keys(Shared& S, int n, int k) {
 
 // The k-th largest of n > k keys, by all threads: where one wave does not hold them, or too many upper
 // halves are the same. A barrier a bit; the counts go round three places, one of them being cleared.
-template <int T>
-__device__ __forceinline__ uint64_t search_wide(Shared& S, int n, int k) {
-  constexpr int R = kTopkCap / T;
+template <int T, class SH>
+__device__ __forceinline__ uint64_t search_wide(SH& S, int n, int k) {
+  constexpr int R = SH::kCap / T;
   const int tid = thread_x();
   uint64_t key[R];
 #pragma unroll
@@ -251,10 +257,10 @@ __device__ __forceinline__ uint64_t search_wide(Shared& S, int n, int k) {
 
 // Cuts the n keys in S.keys to the k largest, in order; those left over go to `left`. Returns the number
 // kept; S.bound is the k-th's value. All T threads call it.
-template <int T>
-__device__ __forceinline__ int cut(Shared& S, int n, int k, Left& left) {
+template <int T, class SH>
+__device__ __forceinline__ int cut(SH& S, int n, int k, Left& left) {
   const int tid = thread_x();
-  constexpr int kMost = T < kRankMost ? T : kRankMost;
+  constexpr int kMost = SH::kRank;
   const uint64_t* from = S.keys;
   int m = n;  // keys that are put in order
   left = Left{};
@@ -308,8 +314,8 @@ __device__ __forceinline__ int cut(Shared& S, int n, int k, Left& left) {
 }
 
 // Joins the threads' sums; the first wave has the result.
-template <int T>
-__device__ void join_rest(Shared& S, Rest& rest) {
+template <int T, class SH>
+__device__ void join_rest(SH& S, Rest& rest) {
   const int tid = thread_x();
   wave_lse(rest.ref, rest.sum);
   if ((tid & 63) == 0) {
@@ -325,8 +331,8 @@ __device__ void join_rest(Shared& S, Rest& rest) {
 }
 
 // Writes a row's answer: the first `kept` keys (an entry that is not there: index -1) and the sum.
-template <int T>
-__device__ void write_row(const TopkParams& P, const Shared& S, int row, int kept, const Rest& rest) {
+template <int T, class SH>
+__device__ void write_row(const TopkParams& P, const SH& S, int row, int kept, const Rest& rest) {
   for (int i = thread_x(); i < P.k; i += T) {
     const uint64_t key = i < kept ? S.keys[i] : 0;
     P.values[(int64_t)row * P.k + i] = key ? key_value((uint32_t)(key >> 32)) : kNegInf;
@@ -339,8 +345,8 @@ __device__ void write_row(const TopkParams& P, const Shared& S, int row, int kep
 }
 
 // One vector: onto the list, or into the sum.
-template <int EPV>
-__device__ __forceinline__ void take(Shared& S, float bound, Low& low, const u32x4& raw, const float (&x)[EPV], int v) {
+template <int EPV, class SH>
+__device__ __forceinline__ void take(SH& S, float bound, Low& low, const u32x4& raw, const float (&x)[EPV], int v) {
   float m = x[0];
 #pragma unroll
   for (int e = 1; e < EPV; ++e) m = fmaxf(m, x[e]);
@@ -348,7 +354,7 @@ __device__ __forceinline__ void take(Shared& S, float bound, Low& low, const u32
   if (__builtin_amdgcn_ballot_w64(cand)) {
     if (cand) {
       const int at = atomicAdd(&S.listed, 1);
-      if (at < kListMost) {
+      if (at < SH::kList) {
         S.list[at] = (uint32_t)v;
         S.listed_raw[at] = raw;
       }
@@ -362,14 +368,16 @@ __device__ __forceinline__ void take(Shared& S, float bound, Low& low, const u32
 
 // The vectors that take() listed, one per thread, once more: elements go into the buffer or to thread `rest`,
 // in batches of threads, the buffer being cut before it could run over. All threads.
-template <int EPV, int T>
-__device__ void take_again(Shared& S, float& bound, float was, const Low& none, Rest& rest, const float (&x)[EPV],
+template <int EPV, int T, class SH>
+__device__ void take_again(SH& S, float& bound, float was, const Low& none, Rest& rest, const float (&x)[EPV],
                            int first, int end, int& n, int k) {
   float m = x[0];
 #pragma unroll
   for (int e = 1; e < EPV; ++e) m = fmaxf(m, x[e]);
+  constexpr int kBatch = SH::kCap / 16;  // threads that append between two looks at the buffer
+  static_assert(kBatch % 64 == 0 && kTopkMax + kBatch * 8 <= SH::kCap, "a batch fits behind the k largest");
   for (int b = 0; b < T / kBatch; ++b) {
-    if (n + kBatch * EPV > kTopkCap) {
+    if (n + kBatch * EPV > SH::kCap) {
       Left left;
       n = cut<T>(S, n, k, left);
       if (n == k) bound = bound_after_cut(S.bound);
@@ -394,11 +402,12 @@ __device__ void take_again(Shared& S, float& bound, float was, const Low& none, 
 // One workgroup of T threads per (row, segment); H vectors per thread are held. M: maxima that the first
 // bound is found from.
 template <bool BF16, int T, int H, int M>
-__global__ void __launch_bounds__(T, T == 512 ? 6 : 3) k_topk(TopkParams P) {
+__global__ void __launch_bounds__(T, T == 1024 ? 4 : 6) k_topk(TopkParams P) {
   using V = Vec<BF16>;
   constexpr int EPV = V::EPV;
   constexpr int U = kLoose;
-  __shared__ Shared S;
+  using SH = Shared<T>;
+  __shared__ SH S;
   const int tid = thread_x();
   const int row = group_x(), seg = group_y();
   const int v0 = seg * P.seg_vec, n_vec = min(P.seg_vec, P.nvec - v0), k = P.k;
@@ -488,7 +497,7 @@ __global__ void __launch_bounds__(T, T == 512 ? 6 : 3) k_topk(TopkParams P) {
     const int listed = S.listed;
     int total = n;
     Low more = low;  // with the listed vectors' elements
-    if (listed <= kListMost) {
+    if (listed <= SH::kList) {
       for (int i = tid; i < listed; i += T) {
         const int v = (int)S.list[i];
         float x[EPV];
@@ -499,7 +508,7 @@ __global__ void __launch_bounds__(T, T == 512 ? 6 : 3) k_topk(TopkParams P) {
           if (first + e < end) {
             if (x[e] >= bound) {
               const int at = atomicAdd(&S.count, 1);
-              if (at < kTopkCap) S.keys[at] = make_key(x[e], first + e);
+              if (at < SH::kCap) S.keys[at] = make_key(x[e], first + e);
             } else {
               more.units += (uint64_t)(more.term(x[e]) * kUnit);
             }
@@ -509,7 +518,7 @@ __global__ void __launch_bounds__(T, T == 512 ? 6 : 3) k_topk(TopkParams P) {
       total = S.count;
     }
     lds_barrier();
-    const bool fits = listed <= kListMost && total <= kTopkCap;
+    const bool fits = listed <= SH::kList && total <= SH::kCap;
     if (tid == 0) {
       S.listed = 0;
       if (!fits) S.count = n;
@@ -539,7 +548,7 @@ __global__ void __launch_bounds__(T, T == 512 ? 6 : 3) k_topk(TopkParams P) {
       g1 = g0 + kGroup * U * T;
     }
     if (!again) seen = kNegInf;
-    if (last || n > kTopkCap / 2 || (!fits && n > k)) {
+    if (last || n > SH::kCap / 2 || (!fits && n > k)) {
       n = cut<T>(S, n, k, left);
       if (n == k && !last) bound = bound_after_cut(S.bound);
     }
@@ -586,7 +595,7 @@ __global__ void __launch_bounds__(T, T == 512 ? 6 : 3) k_topk(TopkParams P) {
 // the threads' maxima are put in order. The others are added to the sums by the threads that loaded them.
 __global__ void __launch_bounds__(kThreads) k_topk_merge(TopkParams P) {
   constexpr int T = kThreads, R = kTopkCap / T;
-  __shared__ Shared S;
+  __shared__ SharedOf<kTopkCap, 1, 256> S;
   const int tid = thread_x(), row = group_x(), k = P.k;
   const int total = P.n_seg * k;
   const uint64_t* keys = P.seg_keys + (int64_t)row * total;
