@@ -657,6 +657,13 @@ constexpr int kFewK = 128;
 // is faster, several smaller ones hide each other's waits (256 rows of 151936 bf16 30 against 35 us, 384
 // rows 51 against 42 us).
 constexpr int kOneEach = 256;
+// A workgroup of 256 threads holds 2048 vectors. Of rows more than six to a CU it takes longer ones too, by
+// streaming the rest, as more of them hide each other's ends (8192 rows of 32003 bf16, k 64: 120 us, 153 with
+// 512 threads, 2048 rows 41 and 46, 512 rows 21 and 18); the bound that it finds in the part it holds is too
+// low for long rows or lists (8192 rows of 151936 bf16, k 64: 443 and 418 us; of 32003 fp32, k 128: 256 and 232).
+constexpr int kManyRows = 1536;
+constexpr int kManyVec = 8192;
+constexpr int kManyK = 64;
 // A row is split if the rows are few, long, and the lists short: one row of 151936 fp32 logits, k 64, 18
 // split against 26 us whole (32 rows 23 against 28, 64 rows 31 against 28), but 13 us whole against 17
 // with 12565 vectors and 36 against 60 with k 256, since joining the segments costs a launch and their
@@ -674,7 +681,8 @@ hipError_t launch(const TopkParams& p, hipStream_t s) {
 template <bool BF16>
 hipError_t launch_rows(const TopkParams& p, hipStream_t s) {
   const bool few = p.k <= kFewK;
-  if (p.seg_vec <= 256 * 8 && few) return launch<BF16, 256, 8, 256>(p, s);
+  const int narrow = p.n_rows > kManyRows && p.k <= kManyK ? kManyVec : 256 * 8;
+  if (p.seg_vec <= narrow && few) return launch<BF16, 256, 8, 256>(p, s);
   if (p.seg_vec > 512 * 10 && p.n_rows <= kOneEach)
     return few ? launch<BF16, 1024, 19, 256>(p, s) : launch<BF16, 1024, 19, 512>(p, s);
   return few ? launch<BF16, 512, 10, 256>(p, s) : launch<BF16, 512, 10, 512>(p, s);

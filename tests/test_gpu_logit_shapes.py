@@ -51,7 +51,7 @@ def _topk_rows(kind, V, rng):
 @pytest.mark.parametrize("rows,V,dtype,k", [
     (3, 262144, "f32", 128), (30, 140000, "bf16", 20), (47, 66000, "f32", 1), (2, 70001, "f32", 129),
     (200, 262144, "bf16", 64), (60, 100003, "f32", 200), (400, 60000, "bf16", 64), (300, 33333, "f32", 256),
-    (300, 40000, "bf16", 128), (500, 16000, "bf16", 100), (65, 8192, "f32", 7), (70, 2500, "f32", 256)])
+    (300, 40000, "bf16", 128), (1600, 30000, "bf16", 33), (1540, 33333, "f32", 64), (500, 16000, "bf16", 100), (65, 8192, "f32", 7), (70, 2500, "f32", 256)])
 def test_top_lists(lib, kind, rows, V, dtype, k):
     base = _topk_rows(kind, V, np.random.default_rng(rows + V + k)).astype(np.float32)
     x = base[np.arange(rows) % 4]
