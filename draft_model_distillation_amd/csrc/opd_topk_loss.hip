@@ -553,11 +553,14 @@ constexpr int kShortVecBwd = 16384;
 // Workgroups of segments that few rows are split for: more of them read the lists and join the sums once
 // more (16 rows of 151936 bf16 fused 10.8 us, with 512 workgroups 12.1, with 1024 15.8).
 constexpr int kSplitGroups = 256;
-// The fused call holds a row of up to 4096 vectors in 256 threads (32003 bf16, 2048 rows: 56 us, 61 with
-// 512). Longer ones take 512, two workgroups to a CU whose waits hide each other, though half of a long
-// row is read again (8192 rows of 151936 bf16 996 us, 1050 with 1024); 1024 where each row has a CU to
-// itself (256 rows 37 us, 40 with 512) or what 512 threads do not hold is most of the row (2048 rows of
-// 151936 fp32 487 us, 560 with 512).
+// The fused call holds a row of up to 1024 vectors in 128 threads where there are many, as each row ends with
+// one wave's arithmetic on its classes and more workgroups hide it (8192 rows of 1000 fp32 26 us, 34 with 256,
+// 47 with 256 that have registers for 16 vectors; 512 rows of 8000 bf16 10.2 us, 8.8 with 256), and one of up to
+// 4096 in 256 (32003 bf16, 2048 rows: 56 us, 61 with 512). Longer ones take 512, two workgroups to a CU whose
+// waits hide each other, though half of a long row is read again (8192 rows of 151936 bf16 996 us, 1050 with
+// 1024); 1024 where each row has a CU to itself (256 rows 37 us, 40 with 512) or what 512 threads do not hold
+// is most of the row (2048 rows of 151936 fp32 487 us, 560 with 512).
+constexpr int kManyRows = 1024;
 constexpr int kOneEach = 256;
 constexpr int kHoldVec = 28672;
 
@@ -603,9 +606,12 @@ hipError_t launch_long(const TopkLossParams& p, hipStream_t s) {
 
 template <bool BF16, bool OUT_BF16>
 hipError_t launch_fused(const TopkLossParams& p, hipStream_t s) {
-  if (p.n_rows >= kHoldRows)
-    return p.nvec <= 256 * 16 ? launch_hold<BF16, OUT_BF16, kFused, 256, 16>(p, s)
-                              : launch_long<BF16, OUT_BF16, kFused>(p, s);
+  if (p.n_rows >= kHoldRows) {
+    if (p.nvec <= 128 * 8 && p.n_rows > kManyRows) return launch_hold<BF16, OUT_BF16, kFused, 128, 8>(p, s);
+    if (p.nvec <= 256 * 8) return launch_hold<BF16, OUT_BF16, kFused, 256, 8>(p, s);
+    if (p.nvec <= 256 * 16) return launch_hold<BF16, OUT_BF16, kFused, 256, 16>(p, s);
+    return launch_long<BF16, OUT_BF16, kFused>(p, s);
+  }
   const hipError_t e = launch_sums<BF16>(p, s);
   return e != hipSuccess ? e : launch_grad<BF16, OUT_BF16, true>(p, s);
 }

@@ -68,7 +68,8 @@ def test_top_lists(lib, kind, rows, V, dtype, k):
     (259, 17003, "bf16", "bf16", 64), (259, 17003, "bf16", "f32", 64), (259, 140003, "bf16", "f32", 33),
     (257, 140003, "bf16", "bf16", 256), (258, 232000, "bf16", "bf16", 100), (256, 140003, "bf16", "bf16", 64),
     (300, 60001, "f32", "f32", 64), (300, 9001, "f32", "bf16", 20), (300, 12000, "bf16", "bf16", 20),
-    (130, 120001, "f32", "bf16", 64), (159, 70001, "f32", "f32", 9), (5, 36000, "f32", "f32", 64)])
+    (1100, 1003, "f32", "f32", 33), (1100, 8001, "bf16", "bf16", 256), (1100, 8001, "bf16", "f32", 20),
+    (1100, 3001, "f32", "bf16", 9), (200, 7001, "bf16", "f32", 33), (130, 120001, "f32", "bf16", 64), (159, 70001, "f32", "f32", 9), (5, 36000, "f32", "f32", 64)])
 def test_distillation(lib, kl, rows, V, dtype, dz, k):
     y, z, rng = GL._rows(rows + V, 4, V)
     pick = np.arange(rows) % 4
